@@ -233,7 +233,7 @@ def prepare(case, seed):
     st["total"], st["max_q"], st["max_len"] = total, max(max(news), 1), max(lens)
     if own:
         from mla_latent_kv_23_b200 import mla
-        st["p"] = mla.tree_params(st["q"], st["cache"], st["table"], st["seqlens"], st["cu"], st["mask"], st["u"], st["lse"], case["page"], D_R, SCALE, st["max_q"])
+        st["p"] = mla.tree_params(st["q"], st["cache"], st["table"], st["seqlens"], st["cu"], st["mask"], st["u"], st["lse"], case["page"], D_R, SCALE)
         st["ws"] = torch.empty(mla.mla_decode_tree_workspace_size(st["p"]), dtype=torch.uint8, device=DEV)
     return st
 
