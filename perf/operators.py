@@ -174,9 +174,6 @@ def prepare(case, seed):
         st["slots"] = torch.randperm(pool, generator=g, device=DEV)[:t].to(torch.int32)
         st["pos"] = torch.randint(0, 131072, (t,), generator=g, device=DEV).to(torch.int32)
         st["cache"] = _normal((pool, WIDTH), g)
-        if own:
-            from mla_latent_kv_23_b200 import mla
-            st["ws"] = mla.projection_workspace(D_C, D_R, t, DEV)
         return st
     sizes = _sizes(case)
     order = torch.randperm(len(sizes), generator=g, device=DEV).tolist()
@@ -352,7 +349,7 @@ def run(st):
     if own:
         from mla_latent_kv_23_b200 import mla
         if st["op"] == "append":
-            mla.mla_append_latent_slots(st["h"], st["w_dkv"], st["w_kr"], st["slots"], st["pos"], st["cache"], rope_base=ROPE_BASE, workspace=st["ws"])
+            mla.mla_append_latent_slots(st["h"], st["w_dkv"], st["w_kr"], st["slots"], st["pos"], st["cache"], rope_base=ROPE_BASE)
             return {"cache": st["cache"]}
         if st["op"] == "tables":
             mla.mla_build_tables(st["p"])
