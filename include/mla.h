@@ -61,6 +61,9 @@ typedef enum { MLA_DTYPE_BF16 = 0, MLA_DTYPE_FP32 = 1 } mla_dtype;
 #define MLA_DEVFLAG_TIMEOUT 0x4     /* a device-side wait gave up (kernel returned early) */
 #define MLA_DEVFLAG_LAYOUT 0x8      /* a kernel's shared memory was not 1024-byte aligned (it returned at once) */
 #define MLA_DEVFLAG_RANGE 0x10      /* a split row's partial u did not fit fp16 (|value| > 65504): u of that row is wrong */
+#define MLA_DEVFLAG_BAD_TREE 0x20   /* drafted tokens: cu_q out of order or range, or more than 64 in a sequence; a parent that is not an earlier token */
+#define MLA_DEVFLAG_NO_PAGES 0x40   /* mla_build_tables: the free list ran out */
+#define MLA_DEVFLAG_NO_ROOM 0x80    /* mla_build_tables: more new tokens than the outputs hold */
 
 const char* mla_status_string(mla_status s);
 
@@ -373,6 +376,177 @@ mla_status mla_output_projection(const void* x, mla_dtype x_dtype, const void* W
  */
 mla_status mla_merge_partials(const void* u_parts, const float* lse_parts, void* u, float* lse,
                               int R, int rows, int d_c, mla_dtype dtype, void* stream);
+
+/*
+ * Latent append through a slot map: mla_append_latent's row for every new
+ * token, at a cache row that need not be the token's position (drafted tokens
+ * of one depth share a position but not a row):
+ *   kv_cache[slots[t]] = [ W_DKV . h[t]  ||  RoPE(W_KR . h[t], pos[t]) ]
+ *   h         [T, d_model]            device, read
+ *   W_DKV     [d_c, d_model]          device, read
+ *   W_KR      [d_R, d_model]          device, read
+ *   slots,pos [T] int32               device, read (as mla_build_tables makes them)
+ *   kv_cache  [cache_rows, d_c + d_R] device, written (only the rows in slots)
+ * A token with slots[t] < 0 has no row and is skipped; one at or past
+ * cache_rows is skipped and raises MLA_DEVFLAG_BAD_PAGE.  Slots must differ
+ * from each other.  d_c and d_R are multiples of 8.
+ * bf16: tensor cores (d_model a multiple of 64), fp32 accumulation, any T in
+ * one launch, no workspace; fp32: CUDA cores.
+ */
+mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void* W_KR,
+                                   const int* slots, const int* pos, void* kv_cache, int cache_rows,
+                                   int T, int d_model, int d_c, int d_R, float rope_base,
+                                   mla_dtype dtype, void* stream);
+
+/*
+ * Block tables and slot maps of a serving step, built on the GPU from the
+ * requests' lengths (no host copy of a length is needed, so a step can be
+ * captured into a CUDA graph).  Request b has ctx_lens[b] cached tokens and
+ * new_lens[b] new ones (drafted tokens, a prompt, or none).  With
+ * have_b = ceil(ctx_b / page_size) (or pages_held[b], if given: pages that the
+ * request already has, e.g. of drafted tokens that were not accepted) and
+ * want_b = max(have_b, ceil((ctx_b + new_b) / page_size)):
+ *   block_table[b][k] = free_pages[free_used + sum_{a<b} (want_a - have_a) + k - have_b]
+ *                       for have_b <= k < want_b; other entries stay as they are
+ *   free_used_out = free_used + sum_b (want_b - have_b)
+ *   seqlens[b] = ctx_b + new_b;  pages_held_out[b] = want_b
+ *   cu_new[b] = sum_{a<b} new_a  (cu_new[B] is the total)
+ * and for the new token t = cu_new[b] + i:
+ *   seq_ids[t] = b
+ *   slots[t]   = block_table[b][(ctx_b + i) / page_size] * page_size + (ctx_b + i) % page_size
+ *   pos[t]     = ctx_b + i
+ * With `parents` (parents[t] < i: the drafted token that token i of its request
+ * follows, or -1) a request of up to 64 new tokens is a tree: pos[t] = ctx_b +
+ * the token's depth, which is its RoPE position, and bit k of tree_mask[t] is
+ * set for k = i and the tokens on its branch before it.  Tokens of a request
+ * of more than 64 are a prompt: their parents are not read, tree_mask[t] = 0.
+ * Entries of seq_ids, pos, slots and tree_mask past the total are not written.
+ *
+ * Device flags: MLA_DEVFLAG_BAD_SEQLEN (a negative length, one past the block
+ * table, pages_held below have_b or above the block table: the request gets no
+ * tokens and seqlens[b] = 0), MLA_DEVFLAG_NO_PAGES (the free list ran out, or
+ * free_used is outside [0, n_free]: block-table entry -1, slots[t] = -1),
+ * MLA_DEVFLAG_BAD_PAGE (a page id outside [0, num_pages): slots[t] = -1),
+ * MLA_DEVFLAG_BAD_TREE (parents[t] < -1 or >= i: the token starts a branch),
+ * MLA_DEVFLAG_NO_ROOM (the total exceeds max_tokens; the tokens past it are
+ * dropped, cu_new counts them).
+ * Inputs and outputs must not share a buffer (block_table is extended in
+ * place).  B <= 16384.  Pointers 16-byte aligned.  One launch.
+ */
+typedef struct {
+  const int* ctx_lens;      /* [B] int32 device                                     */
+  const int* new_lens;      /* [B] int32 device                                     */
+  const int* pages_held;    /* [B] int32 device, or NULL                            */
+  int* block_table;         /* [B, max_pages_per_seq] int32 device, read and written */
+  const int* free_pages;    /* [n_free] int32 device: page ids                      */
+  const int* free_used;     /* [1] int32 device: entries of free_pages already taken */
+  int* free_used_out;       /* [1] int32 device, written                            */
+  int* seqlens;             /* [B] int32 device, written                            */
+  int* cu_new;              /* [B + 1] int32 device, written                        */
+  int* pages_held_out;      /* [B] int32 device, written; NULL exactly if pages_held is */
+  int* seq_ids;             /* [max_tokens] int32 device, written                   */
+  int* pos;                 /* [max_tokens] int32 device, written                   */
+  int* slots;               /* [max_tokens] int32 device, written                   */
+  const int* parents;       /* [max_tokens] int32 device, or NULL                   */
+  int64_t* tree_mask;       /* [max_tokens] device, written; NULL exactly if parents is */
+  int B, max_pages_per_seq, n_free, max_tokens, page_size, num_pages;
+} mla_tables_params;
+
+mla_status mla_build_tables(const mla_tables_params* p, void* stream);
+
+/*
+ * Attention of drafted trees over the paged latent cache: mla_decode for the
+ * verification step of speculative decoding, where every sequence has up to 64
+ * drafted tokens that branch.  The formulas are mla_decode's ("MLA deep
+ * compression", absorption and decoupled-RoPE sections); only what a row sees
+ * differs.  Sequence b has n_b = cu_q[b + 1] - cu_q[b] drafted tokens, rows
+ * cu_q[b] .. cu_q[b + 1] - 1 of q, u, lse and tree_mask; they are the last n_b
+ * of its seqlens[b] cached tokens, in the same order (mla_append_latent_slots
+ * wrote them there).  For token t = cu_q[b] + r and head i, over the positions
+ *   j < seqlens[b] - n_b                                (the context), and
+ *   j = seqlens[b] - n_b + k with bit k of tree_mask[t] (r's branch; r itself
+ *                                                        only if bit r is set):
+ *     s_j = q[t,i,:d_c] . c_j + q[t,i,d_c:] . kR_j
+ *     u[t,i,:] = sum_j softmax(softmax_scale * s)_j c_j;  lse[t,i] as mla_decode
+ * A token that sees nothing gets u = 0 and lse = -inf.  Cache rows that a token
+ * does not see never enter its result, whatever they hold (rows past
+ * seqlens[b], and the drafted tokens of other branches, may hold infinities
+ * and NaN).  mla_build_tables makes cu_q, seqlens and tree_mask of a tree; a
+ * chain of drafted tokens is the mask (2 << r) - 1.
+ *
+ * Rows of q, u and lse past cu_q[B] are not read for any result and not
+ * written.  Sequences without drafted tokens (n_b = 0) are skipped.  What the
+ * host cannot see raises a device flag: cu_q out of order or outside [0, T],
+ * or n_b > 64 (MLA_DEVFLAG_BAD_TREE; the sequences on either side of the wrong
+ * entry are skipped, their rows keep their values), seqlens[b] < n_b or past the block table
+ * (MLA_DEVFLAG_BAD_SEQLEN; u = 0 and lse = -inf), page ids out of range
+ * (MLA_DEVFLAG_BAD_PAGE; page 0 is read instead).
+ *
+ * Softmax statistics, sums and the partial results of rows split over KV chunks
+ * are fp32; the softmax weights are rounded to bf16 for the product with C, and
+ * u is normalised by the sum of the rounded weights.
+ * Supported: bf16, d_c = 512, d_R = 64, n_h <= 128.  All pointers 16-byte
+ * aligned; the workspace is 256-byte aligned scratch that keeps no state.
+ * Calls that share a workspace must be ordered on the GPU.
+ */
+typedef struct {
+  const void* q;            /* [T, n_h, d_c + d_R] device; latent part first, then RoPE         */
+  const void* kv_cache;     /* [num_pages * page_size, d_c + d_R] device; row = c || k^R        */
+  const int* block_table;   /* [B, max_pages_per_seq] int32 device                              */
+  const int* seqlens;       /* [B] int32 device; cached tokens with the drafted ones            */
+  const int* cu_q;          /* [B + 1] int32 device; prefix sums of the drafted tokens          */
+  const int64_t* tree_mask; /* [T] device; bit k: the token sees drafted token k of its sequence */
+  void* u;                  /* [T, n_h, d_c] device, written; dtype, or fp32 if u_fp32          */
+  float* lse;               /* [T, n_h] fp32 device, written; may be NULL                       */
+  int B;                    /* sequences; 0 is a no-op                                          */
+  int T;                    /* rows that q, u, lse and tree_mask hold; 0 is a no-op             */
+  int n_h, d_c, d_R;
+  int page_size, max_pages_per_seq, num_pages;
+  float softmax_scale;
+  mla_dtype dtype;          /* of q, kv_cache and u                                             */
+  int num_splits;           /* KV chunks the whole batch is cut into; 0 = one per SM pair       */
+  int u_fp32;
+} mla_tree_params;
+
+mla_status mla_decode_tree_workspace_size(const mla_tree_params* p, size_t* bytes);
+mla_status mla_decode_tree(const mla_tree_params* p, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * After verification: keeps the accepted branch of every drafted tree in the
+ * cache.  Sequence b has the n_b = cu_q[b + 1] - cu_q[b] drafted tokens of
+ * mla_decode_tree as the last of its seqlens[b] cached ones; accepted[b] is the
+ * last accepted one (its index within the tree; -1: none).  With k_0 < k_1 < ...
+ * < k_{m-1} the set bits of tree_mask[cu_q[b] + accepted[b]] below n_b:
+ *   the cache row of drafted token k_i moves to the place of drafted token i
+ *   seqlens_out[b] = seqlens[b] - n_b + m
+ *   path[cu_q[b] + i] = k_i for i < m, -1 for m <= i < n_b
+ * so the kept tokens follow the context, their RoPE positions (depths) being
+ * their places, and `path` gathers whatever else belongs to them.  Whole rows are
+ * moved as they are; rows of the cache that are no target keep their values.
+ * seqlens_out may be seqlens.
+ * Device flags: MLA_DEVFLAG_BAD_TREE (cu_q out of order or outside [0, T], more
+ * than 64 drafted tokens, accepted[b] outside [-1, n_b): nothing is kept),
+ * MLA_DEVFLAG_BAD_SEQLEN (seqlens[b] < n_b or past the block table: nothing is
+ * done, seqlens_out[b] = seqlens[b]), MLA_DEVFLAG_BAD_PAGE (the row is not
+ * moved).
+ */
+typedef struct {
+  void* kv_cache;           /* [num_pages * page_size, width] device, read and written */
+  const int* block_table;   /* [B, max_pages_per_seq] int32 device                  */
+  const int* seqlens;       /* [B] int32 device                                     */
+  const int* cu_q;          /* [B + 1] int32 device                                 */
+  const int64_t* tree_mask; /* [T] device                                           */
+  const int* accepted;      /* [B] int32 device                                     */
+  int* seqlens_out;         /* [B] int32 device, written                            */
+  int* path;                /* [T] int32 device, written                            */
+  int B, T;
+  int width;                /* d_c + d_R; a row is a multiple of 16 bytes           */
+  int page_size, max_pages_per_seq, num_pages;
+  mla_dtype dtype;          /* of kv_cache                                          */
+} mla_accept_params;
+
+mla_status mla_accept_tree(const mla_accept_params* p, void* stream);
 
 /*
  * Self-test of the bounded device-side wait.  Launches one kernel that

@@ -11,8 +11,12 @@
 #include <functional>
 #include <mutex>
 
+#include "abi_common.h"
+#include "append_slots.h"
 #include "internal.h"
 #include "mla.h"
+#include "tables.h"
+#include "tree.h"
 
 namespace mla {
 
@@ -21,29 +25,16 @@ __device__ int g_device_flags;
 
 int decode_sm100_prepare();
 
+EncodeTiledFn g_encode = nullptr;
+
 namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  bool ready = false;
-  int sm_count = 0;
-  int cc_major = 0, cc_minor = 0;
-  int max_clusters = 0;  // co-resident 2-CTA clusters of the DeepSeek-V3-shape kernel
-  bool small_tc = false;  // the small-latent tensor-core kernel is usable
-  bool up_proj_tc = false;
-  bool wgemm_tc = false;  // the weight-streaming projection kernel is usable
-  int* flags = nullptr;  // device address of g_device_flags
-};
-
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_mutex;
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
+}  // namespace
 
 mla_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
@@ -68,9 +59,12 @@ mla_status device_info(const DeviceInfo** out) {
     if ((e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.flags), g_device_flags)) != cudaSuccess)
       return cuda_status(e);
     d.max_clusters = (d.cc_major == 10) ? decode_sm100_prepare() : 0;
+    d.tree_clusters = (d.cc_major == 10) ? tree_sm100_prepare() : 0;
     d.small_tc = (d.cc_major == 10) && decode_small_sm100_prepare() != 0;
     d.up_proj_tc = (d.cc_major == 10) && up_proj_sm100_prepare() != 0;
     d.wgemm_tc = (d.cc_major == 10) && wgemm_sm100_prepare() != 0;
+    d.append_tc = (d.cc_major == 10) && append_slots_prepare() != 0;
+    if ((e = tables_prepare()) != cudaSuccess) return cuda_status(e);
     if (g_encode == nullptr) {
       cudaDriverEntryPointQueryResult q;
       void* fn = nullptr;
@@ -86,11 +80,7 @@ mla_status device_info(const DeviceInfo** out) {
   return MLA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool valid_dtype(mla_dtype d) { return d == MLA_DTYPE_BF16 || d == MLA_DTYPE_FP32; }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
 
 mla_status validate_decode(const mla_decode_params* p) {
   if (p == nullptr) return MLA_ERR_INVALID_ARG;

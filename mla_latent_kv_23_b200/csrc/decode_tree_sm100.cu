@@ -1,0 +1,952 @@
+// Attend stage of mla_decode_tree on the 5th-generation tensor cores (sm_100a)
+// at the DeepSeek-V3 shape: latent d_c = 512, RoPE key d_R = 64, bf16.
+//
+// Math ("MLA deep compression", absorption section, both equations, and its
+// decoupled-RoPE section), for token r of a tree of n drafted tokens that are
+// the last n of a sequence's L cached ones, and for every head:
+//     s_j = q . [c_j || k^R_j],  seen where j < L - n or bit j - (L - n) of mask_r
+//     u   = sum_j softmax(scale s)_j c_j
+// The n n_h query rows of a sequence are flat (token-major) and taken in
+// blocks of 128: all rows of a block share every cached row, so they are the M
+// dimension of two dense contractions per 64-token tile,
+//     S = Q . [C || K^R]^T      (K = 576)
+//     O = O * alpha + P . C     (N = 512 latent)
+// with an online softmax between them; u = O / l at the end.  Few heads fill a
+// block with several tokens of the tree, so that a cached row is read once
+// for them.
+//
+// What bounds it: 128 rows take 278.5 kflop for each 1152-byte cached row,
+// 242 flop/B, the ridge of this part: at one block a sequence the HBM and the
+// tensor roofline meet, at more blocks the tile comes from L2 and the tensor
+// cores bound it.  O of 128 rows and 512 columns in fp32 fills the tensor
+// memory of one SM, so a pair of CTAs (one 2-CTA cluster) shares a block, and
+// the operands are split as in the decode kernel of this shape:
+//  * CTA r loads, for every cached row, latent columns [128r, 128r + 128) and
+//    [256 + 128r, 256 + 128r + 128) plus RoPE columns [32r, 32r + 32).
+//  * CTA r owns rows [64r, 64r + 64) of the block and their O in its TMEM.
+//  * P . C is one paired MMA (cta_group::2) per 16 tokens and 256 columns.
+//  * S is a paired MMA with M = 256: rows (query row i, column half j) against
+//    B = [CTA 0's columns of the tile | CTA 1's]; row (i, j) counts against
+//    half j, so half of the products are discarded and one shuffle adds the two
+//    partial scores.  Per tile 1673 tensor cycles are issued where 1095 would
+//    do; passing data between the CTAs instead costs more than it saves.
+//
+// The mask is one 64-bit word per token: a tile that reaches into the drafted
+// tokens shifts it to the tile's positions.  A drafted token's cache row may
+// hold infinities or NaN that a row which does not see it must not meet (0 x
+// NaN in P . C): every row's raw score of such a token is then non-finite, so
+// the softmax finds it there and clears the non-finite values of that cache
+// row in shared memory before P . C; rows that see the token get NaN by their
+// weight.
+//
+// TMEM per CTA (512 columns): S 2 x 128 (double-buffered) | O 256.
+// Shared memory per CTA: Q (128 rows x 288 values, the S operand A) 72 KB;
+// 4 tile stages of 36 KB; P (64 rows x 64 tokens bf16) as two 32-token halves:
+// tokens 0-31 in the tile's own RoPE block (free once S of the tile is done),
+// tokens 32-63 in a two-slot 4 KB ring.
+//
+// Roles (384 threads): warp 0 = TMA producer; warp 1 = S issuer and warp 2 =
+// P . C issuer (even CTA); warp 3 = relay (the segment's queries, rows past a
+// sequence's end zeroed, signals to the even CTA); warps 4-11 = softmax, two
+// groups of four that take alternate tiles.
+//
+// Epilogue: u = O / l leaves TMEM through the query area (free once the
+// segment's last S is done) by TMA stores of whole 128-byte lines, or row by
+// row where fewer than a warp's 32 rows exist (the rows behind belong to the
+// next sequence).  Pieces of split blocks are written in fp32.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "sm100_ptx.cuh"
+#include "tree.h"
+#include "tree_schedule.cuh"
+
+namespace mla {
+namespace {
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpAlloc = 2, kWarpRelay = 3, kWarpSoftmax0 = 4;
+constexpr int kStages = 4;
+constexpr int kDc = 512;
+
+constexpr uint32_t kKvBlk = 64 * 128;                    // tile: 64 rows x 64 cols, SW128
+constexpr uint32_t kKvRope = 64 * 64;                    // tile: 64 rows x 32 cols, SW64
+constexpr uint32_t kStageBytes = 4 * kKvBlk + kKvRope;   // 36864
+constexpr uint32_t kQBlk = 128 * 128;                    // Q: 128 rows x 64 cols, SW128
+constexpr uint32_t kQRope = 128 * 64;                    // Q: 128 rows x 32 cols, SW64
+constexpr uint32_t kQBytes = 4 * kQBlk + kQRope;         // 73728
+constexpr uint32_t kPHalf = 64 * 64;                     // 64 rows x 32 tokens bf16, SW64
+
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffKv = kOffQ + kQBytes;
+constexpr uint32_t kOffP = kOffKv + kStages * kStageBytes;   // [2] second halves of P
+constexpr uint32_t kOffMax = kOffP + 2 * kPHalf;             // float [2 tile parity][64 rows]
+constexpr uint32_t kOffSum = kOffMax + 2 * 64 * 4;           // float [2 kind][2 group][64 rows]
+constexpr uint32_t kOffScratch = kOffSum + 2 * 2 * 64 * 4;    // 16 words written by the odd CTA's signals
+constexpr uint32_t kOffBar = kOffScratch + 64;
+
+// Barriers of the even CTA that the odd CTA signals ("paired" below) count
+// the even CTA's own arrivals, and the odd CTA's signals as 4-byte
+// transactions (st.async) that one of the even CTA's arrivals announces.
+enum Bar {
+  LOCAL_FULL = 0,                  // [stage] this CTA's TMA bytes of a stage (tail tiles)
+  KV_FULL = LOCAL_FULL + kStages,  // [stage] even CTA: both CTAs' stage ready; full tiles count
+                                   //     both CTAs' TMA bytes, tail tiles the relays' signals
+  KV_EMPTY = KV_FULL + kStages,    // [stage] P . C of the stage's tile done (paired commit)
+  S_FULL = KV_EMPTY + kStages,     // [2] per S buffer (paired commit)
+  S_EMPTY = S_FULL + 2,            // [2] even CTA, paired: softmax warps read the S buffer
+  P_FULL = S_EMPTY + 2,            // [2] even CTA, paired: softmax warps wrote P
+  PV_DONE = P_FULL + 2,            // [2] (paired commit)
+  Q_LOCAL = PV_DONE + 2,           // this CTA's query bytes
+  Q_FULL,                          // even CTA, paired: both queries in place (relays)
+  Q_EMPTY,                         // last S of a segment done (paired commit)
+  DEC,                             // [2] per softmax group: its 4 warps decided a tile's maximum
+  GRP = DEC + 2,                   // the 8 softmax warps of this CTA
+  EPI_FREE,                        // the 8 softmax warps' output stores have read the query area
+  MMA_FINAL,                       // even CTA: all S issued so far are complete
+  MMA_FINAL_PV,                    // even CTA: all P . C issued so far are complete
+  BAR_COUNT
+};
+constexpr uint32_t kOffTmemSlot = kOffBar + BAR_COUNT * 8;
+constexpr uint32_t kSmemUsed = kOffTmemSlot + 16;
+constexpr size_t kSmemBytes = kSmemUsed;  // the base is 1024-byte aligned (checked at entry)
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0;     // 2 x 128 columns
+constexpr uint32_t kTmemO = 256;   // 2 x 128 columns (latent blocks 0-255, 256-511)
+constexpr float kRescaleThreshold = 30.0f;  // log2 units: rescale O only if the max grows by > 2^30
+constexpr int kPrefetchAhead = 4;           // tiles between an L2 prefetch and the tile's TMA load
+constexpr uint16_t kBothCtas = 3;
+
+static_assert(kOffKv % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, "align");
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+// First latent column of 64-column block kc (0..3) of the columns CTA `half`
+// owns; the RoPE columns of that CTA start at 512 + 32 half.
+__device__ __forceinline__ int lat_col(int kc, int half) {
+  return (kc >> 1) * 256 + half * 128 + (kc & 1) * 64;
+}
+
+struct Params {
+  TreeMaps maps;
+  const __nv_bfloat16* q;   // for L2 prefetch of the next segment's rows
+  const __nv_bfloat16* kv;  // for L2 prefetch of tiles ahead of their loads
+  const int* block_table;
+  const int* seqlens;
+  const int* cu_q;
+  const unsigned long long* mask;
+  const int* rec;
+  float* part_lse;
+  void* u;
+  float* lse;
+  int* err;
+  int B, T, n_h, max_pages, page_size, num_pages;
+  int out_f32;       // u is fp32 (else bf16)
+  float scale_log2;  // softmax_scale * log2(e)
+};
+
+// 2D tiled store of a shared-memory box; tracked by bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Lane 0 polls (a warp of spinning lanes only adds shared-memory traffic);
+// the shuffle hands the outcome, and the ordering, to the rest of the warp.
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster>(bar, parity, err, MLA_DEVFLAG_TIMEOUT);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// Both phases complete; the two tests of each poll are independent, so their
+// shared-memory latencies overlap.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                           uint32_t par1, int* err) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t t0 = cycles();
+    uint32_t n = 0;
+    while (!(mbar_test_nb(bar0, par0) & mbar_test_nb(bar1, par1))) {
+      if ((++n & 31u) == 0 && cycles() - t0 > kWaitLimitCycles) {
+        atomicOr(err, MLA_DEVFLAG_TIMEOUT);
+        ok = false;
+        break;
+      }
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_sm100_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sbase = smem_u32(smem_raw);
+  uint8_t* base = smem_raw;
+  if (sbase & 1023u) {  // the swizzled layouts need it; nothing has been started yet
+    if (threadIdx.x == 0) atomicOr(p.err, MLA_DEVFLAG_LAYOUT);
+    return;
+  }
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunk = blockIdx.x >> 1;
+  const long long max_len = (long long)p.max_pages * p.page_size;
+  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
+  // Signal a paired barrier of the even CTA: from the even CTA a local
+  // arrival (with `announce`, the one arrival per phase that also expects the
+  // odd CTA's `odd_bytes` of signals); from the odd CTA a non-blocking 4-byte
+  // st.async into scratch word `scratch_word` of the even CTA.
+  auto signal_lead = [&](int i, bool announce, uint32_t odd_bytes, int scratch_word) {
+    if (leader) {
+      if (announce)
+        mbar_arrive_expect_tx(bar(i), odd_bytes);
+      else
+        mbar_arrive(bar(i));
+    } else {
+      st_async_b32(mapa(sbase + kOffScratch + 4u * scratch_word, 0), 0u, mapa(bar(i), 0));
+    }
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(LOCAL_FULL + s), 1);
+      mbar_init(bar(KV_FULL + s), 1);
+      mbar_init(bar(KV_EMPTY + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(S_FULL + i), 1);
+      mbar_init(bar(S_EMPTY + i), 4);
+      mbar_init(bar(P_FULL + i), 4);
+      mbar_init(bar(DEC + i), 4);
+      mbar_init(bar(PV_DONE + i), 1);
+    }
+    mbar_init(bar(Q_LOCAL), 1);
+    mbar_init(bar(Q_FULL), 1);
+    mbar_init(bar(Q_EMPTY), 1);
+    mbar_init(bar(GRP), 8);
+    mbar_init(bar(EPI_FREE), 8);
+    mbar_init(bar(MMA_FINAL), 1);
+    mbar_init(bar(MMA_FINAL_PV), 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpAlloc) {
+    tmem_alloc_pair(sbase + kOffTmemSlot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tmap(&p.maps.kv_lat4);
+    prefetch_tmap(&p.maps.kv_rope);
+  }
+  if (warp == kWarpRelay && lane == 0) {
+    prefetch_tmap(p.maps.has_q4 ? &p.maps.q_lat4 : &p.maps.q_lat);
+    prefetch_tmap(p.maps.has_q4 ? &p.maps.q_rope4 : &p.maps.q_rope);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and TMEM exist before either uses the other's
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kOffTmemSlot);
+  // everything above overlaps the plan kernel; its results are read below
+  pdl_wait_previous();
+  pdl_launch_dependents();
+
+  if (warp == kWarpTma) {
+    // ------------------------------------------------------------ producer
+    // a sequence of one row block reads each of its tiles once: those are
+    // evicted from L2 first; with more blocks other clusters read the same
+    // tiles, from L2 if they are still there
+    const uint64_t pol_once = l2_policy_evict_first(), pol_shared = l2_policy_evict_normal();
+    TreeWalk walk;
+    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    TreeSegment sg;
+    int g = 0;
+    int last_n[kStages], tail_n[kStages];  // uses of LOCAL_FULL per stage
+    for (int s = 0; s < kStages; ++s) last_n[s] = -1, tail_n[s] = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int* bt = p.block_table + (size_t)sg.b * p.max_pages;
+      const int L = sg.seq.L;
+      const uint64_t pol_stream = sg.seq.blocks == 1 ? pol_once : pol_shared;
+      for (int t0 = sg.t0; ok && t0 < sg.t1; t0 += 32) {
+        // each lane fetches the page of one upcoming tile
+        int my_page = 0;
+        if (t0 + lane < sg.t1) {
+          my_page = bt[((t0 + lane) * kTreeTile) / p.page_size];
+          if (my_page < 0 || my_page >= p.num_pages) {
+            atomicOr(p.err, MLA_DEVFLAG_BAD_PAGE);
+            my_page = 0;
+          }
+        }
+        const int n_here = min(32, sg.t1 - t0);
+        for (int i = 0; i < n_here; ++i, ++g) {
+          const int page = __shfl_sync(0xffffffffu, my_page, i);
+          // The tile kPrefetchAhead tiles later goes to L2 now: its TMA load is
+          // issued only when a stage frees (after this tile's P . C), and an
+          // L2 hit then lands in a fraction of the HBM latency, which would
+          // otherwise keep every stage busy that much longer.  A 64-token
+          // tile of one page is 64 x 1152 contiguous bytes; the even CTA
+          // fetches all of it.
+          // At the start of a chunk every SM is already loading its query and
+          // first stages; fetching more then only delays those, so the first
+          // kStages tiles of the chunk prefetch nothing.
+          const int page_ahead = __shfl_sync(0xffffffffu, my_page, (i + kPrefetchAhead) & 31);
+          if (leader && lane == 0 && g >= kStages && i + kPrefetchAhead < n_here) {
+            const int tok_a = (t0 + i + kPrefetchAhead) * kTreeTile;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                p.kv + ((size_t)page_ahead * p.page_size + tok_a % p.page_size) * (kDc + 64));
+            constexpr uint32_t kTile = kTreeTile * (kDc + 64) * 2;
+            for (uint32_t off = 0; off < kTile; off += 16384)
+              bulk_prefetch_l2(src + off, min(16384u, kTile - off));
+          }
+          if (lane == 0) {
+            const int s = g % kStages, n = g / kStages;
+            ok = mbar_wait(bar(KV_EMPTY + s), (n & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT);
+            if (ok) {
+              const int tok = (t0 + i) * kTreeTile;
+              const int y = page * p.page_size + tok % p.page_size;
+              const uint32_t st = sbase + kOffKv + s * kStageBytes;
+              if (L - tok < kTreeTile) {
+                // tail tile: this CTA's relay zeroes the rows past the end
+                // once they land, then signals the even CTA
+                mbar_arrive_expect_tx(bar(LOCAL_FULL + s), kStageBytes);
+                tma_load_4d_hint(st, &p.maps.kv_lat4, bar(LOCAL_FULL + s), 128 * (int)rank, y, 0, 0,
+                                 pol_stream);
+                tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(LOCAL_FULL + s),
+                                 kDc + 32 * (int)rank, y, pol_stream);
+                last_n[s] = tail_n[s]++;
+              } else if (leader) {
+                // full tile: both CTAs' bytes complete on the even CTA's barrier
+                mbar_arrive_expect_tx(bar(KV_FULL + s), 2 * kStageBytes);
+                tma_load_4d_hint(st, &p.maps.kv_lat4, bar(KV_FULL + s), 0, y, 0, 0, pol_stream);
+                tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(KV_FULL + s), kDc, y,
+                                 pol_stream);
+              } else {
+                const uint32_t full = mapa(bar(KV_FULL + s), 0);
+                tma_load_4d_to_pair_hint(st, &p.maps.kv_lat4, full, 128, y, 0, 0, pol_stream);
+                tma_load_2d_to_pair_hint(st + 4 * kKvBlk, &p.maps.kv_rope, full, kDc + 32, y, pol_stream);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+        }
+      }
+    }
+    // wait for this thread's tail copies in flight before the CTA may exit
+    // (full tiles are consumed by the paired MMAs before the final cluster
+    // barrier)
+    if (lane == 0)
+      for (int s = 0; s < kStages; ++s)
+        if (last_n[s] >= 0) mbar_wait(bar(LOCAL_FULL + s), last_n[s] & 1, p.err, MLA_DEVFLAG_TIMEOUT);
+    __syncwarp();
+  } else if (warp == kWarpRelay) {
+    // ------------------------------------------------------------ relay
+    TreeWalk walk;
+    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    TreeSegment sg;
+    int g = 0, seg_i = 0;
+    int tail_n[kStages];  // uses of LOCAL_FULL per stage, in tile order
+    for (int s = 0; s < kStages; ++s) tail_n[s] = 0;
+    bool ok = true;
+    bool q_in_flight = false;
+    while (ok && walk.next(sg)) {
+      // this segment's query rows (i, j) = Q[64 rank + 16 qd + i, columns of
+      // CTA j], stored as row 32 qd + 16 j + i.  Rows past the block's last
+      // belong to the next sequence, or read as zero behind q's end: nothing
+      // of theirs is written.
+      // the query area is free once the previous segment's last S has read
+      // it and its epilogue's output stores (staged there) have left
+      if (seg_i > 0 && !(ok = warp_wait(bar(Q_EMPTY), (seg_i - 1) & 1, p.err) &&
+                              warp_wait(bar(EPI_FREE), (seg_i - 1) & 1, p.err)))
+        break;
+      if (lane == 0) {
+        const int y0 = sg.first + 64 * (int)rank;
+        mbar_arrive_expect_tx(bar(Q_LOCAL), kQBytes);
+        if (p.maps.has_q4) {
+          // one copy per 64-column block: rows 32 qd + 16 j + i at once
+          for (int kc = 0; kc < 4; ++kc)
+            tma_load_4d(sbase + kOffQ + kc * kQBlk, &p.maps.q_lat4, bar(Q_LOCAL), lat_col(kc, 0), 0,
+                        0, y0 >> 4);
+          tma_load_4d(sbase + kOffQ + 4 * kQBlk, &p.maps.q_rope4, bar(Q_LOCAL), kDc, 0, 0, y0 >> 4);
+        } else {
+          for (int qd = 0; qd < 4; ++qd)
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t r0 = static_cast<uint32_t>(32 * qd + 16 * j);
+              for (int kc = 0; kc < 4; ++kc)
+                tma_load_2d(sbase + kOffQ + kc * kQBlk + r0 * 128, &p.maps.q_lat, bar(Q_LOCAL),
+                            lat_col(kc, j), y0 + 16 * qd);
+              tma_load_2d(sbase + kOffQ + 4 * kQBlk + r0 * 64, &p.maps.q_rope, bar(Q_LOCAL),
+                          kDc + 32 * j, y0 + 16 * qd);
+            }
+        }
+      }
+      q_in_flight = true;
+      // the next segment's query rows go to L2 now, so that its TMA load
+      // after this segment's last S is an L2 hit
+      if (lane == 0) {
+        TreeWalk peek = walk;
+        TreeSegment nx;
+        if (peek.next(nx) && nx.rows > 64 * (int)rank) {
+          const __nv_bfloat16* src = p.q + ((size_t)nx.first + 64 * rank) * (kDc + 64);
+          const uint32_t bytes =
+              static_cast<uint32_t>(min(64, nx.rows - 64 * (int)rank)) * (kDc + 64) * 2;
+          for (uint32_t off = 0; off < bytes; off += 16384)
+            bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(src) + off, min(16384u, bytes - off));
+        }
+      }
+      if (!(ok = warp_wait(bar(Q_LOCAL), seg_i & 1, p.err))) break;
+      q_in_flight = false;
+      if (lane == 0) signal_lead(Q_FULL, true, 4u, 8);
+      __syncwarp();
+
+      const int L = sg.seq.L;
+      for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+        const int s = g % kStages;
+        const int rows_valid = L - t * kTreeTile;
+        if (rows_valid >= kTreeTile) continue;  // full tile: no relay
+        if (!(ok = warp_wait(bar(LOCAL_FULL + s), (tail_n[s]++) & 1, p.err))) break;
+        // rows past the sequence end may hold anything; make them zero so
+        // that 0-probability x garbage cannot turn into NaN in P . C
+        uint8_t* tile = base + kOffKv + s * kStageBytes;
+        for (int r = max(rows_valid, 0); r < kTreeTile; ++r) {
+          if (lane < 8)
+            for (int kb = 0; kb < 4; ++kb)
+              *reinterpret_cast<uint4*>(tile + kb * kKvBlk + r * 128 + lane * 16) =
+                  make_uint4(0, 0, 0, 0);
+          if (lane < 4)
+            *reinterpret_cast<uint4*>(tile + 4 * kKvBlk + r * 64 + lane * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) signal_lead(KV_FULL + s, true, 4u, 9);
+        __syncwarp();
+      }
+      ++seg_i;
+    }
+    // a query copy still in flight must land before the CTA may exit
+    if (q_in_flight && lane == 0) mbar_wait(bar(Q_LOCAL), seg_i & 1, p.err, MLA_DEVFLAG_TIMEOUT);
+    __syncwarp();
+  } else if (warp == kWarpMma || warp == kWarpAlloc) {
+    // ------------------------------------------------------------ MMA issuers
+    // Warp 1 issues every S, warp 2 (done allocating) every P . C.  The two
+    // streams touch disjoint TMEM and shared memory, and each commit tracks
+    // only its own thread's MMAs, so a P . C whose P is ready never waits
+    // behind an S being issued (issuing blocks while the tensor pipe's queue
+    // is full) and vice versa.
+    if (leader) {
+      constexpr uint32_t kIdS = idesc_bf16(256, 128, false);
+      constexpr uint32_t kIdPV = idesc_bf16(128, 256, true);
+      TreeWalk walk;
+      walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+      TreeSegment sg;
+      int g0 = 0, seg_i = 0;
+      bool ok = true;
+      // S for global tile g: 16 steps over the latent columns, 2 over RoPE
+      auto issue_s = [&](int g, bool last) {
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t st = sbase + kOffKv + (g % kStages) * kStageBytes;
+          const uint32_t dS = tmem + kTmemS + (g & 1) * 128;
+          uint32_t acc = 0;
+          for (int kc = 0; kc < 4; ++kc)
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t a =
+                  smem_desc(sbase + kOffQ + kc * kQBlk + ks * 32, 16, 1024, kLayoutSW128);
+              const uint64_t b = smem_desc(st + kc * kKvBlk + ks * 32, 16, 1024, kLayoutSW128);
+              umma_f16_ss_pair(dS, a, b, kIdS, acc);
+              acc = 1;
+            }
+          for (int ks = 0; ks < 2; ++ks) {
+            const uint64_t a = smem_desc(sbase + kOffQ + 4 * kQBlk + ks * 32, 16, 512, kLayoutSW64);
+            const uint64_t b = smem_desc(st + 4 * kKvBlk + ks * 32, 16, 512, kLayoutSW64);
+            umma_f16_ss_pair(dS, a, b, kIdS, 1u);
+          }
+          umma_commit_pair(bar(S_FULL + (g & 1)), kBothCtas);
+          if (last) umma_commit_pair(bar(Q_EMPTY), kBothCtas);
+        }
+        __syncwarp();
+      };
+      // O (+)= P . C for global tile g; `first` = first tile of its segment
+      auto issue_pv = [&](int g, bool first) {
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t st = sbase + kOffKv + (g % kStages) * kStageBytes;
+          // P tokens 0-31 sit in the stage's RoPE block (S is done with it),
+          // tokens 32-63 in the second-half ring
+          const uint32_t pa0 = st + 4 * kKvBlk, pa1 = sbase + kOffP + (g & 1) * kPHalf;
+          for (int blk = 0; blk < 2; ++blk)
+            for (int kk = 0; kk < 4; ++kk) {  // 16 tokens per MMA
+              const uint64_t a = smem_desc((kk < 2 ? pa0 : pa1) + (kk & 1) * 32, 16, 512, kLayoutSW64);
+              const uint64_t b =
+                  smem_desc(st + 2 * blk * kKvBlk + kk * 2048, kKvBlk, 1024, kLayoutSW128);
+              umma_f16_ss_pair(tmem + kTmemO + blk * 128, a, b, kIdPV,
+                               (first && kk == 0) ? 0u : 1u);
+            }
+          umma_commit_pair(bar(KV_EMPTY + g % kStages), kBothCtas);
+          umma_commit_pair(bar(PV_DONE + (g & 1)), kBothCtas);
+        }
+        __syncwarp();
+      };
+      // Fixed order per segment: S0 S1 S2, then P.C(j) S(j+3) for every tile
+      // j, so S runs two tiles ahead of P.C and the softmax of tile j has
+      // two S groups of tensor work to hide behind.  Each step polls only the
+      // barriers it needs (a barrier test costs ~150 cycles; re-testing a
+      // ready barrier is not free).
+      const bool s_issuer = warp == kWarpMma;
+      while (ok && walk.next(sg)) {
+        const int n_t = sg.t1 - sg.t0;
+        if (s_issuer) {
+          // S(g) once its stage is loaded and its S buffer has been read
+          if (!(ok = warp_wait(bar(Q_FULL), seg_i & 1, p.err))) break;
+          for (int j = 0; ok && j < n_t; ++j) {
+            const int g = g0 + j;
+            if (!(ok = warp_wait2(bar(KV_FULL + g % kStages), (g / kStages) & 1,
+                                  bar(S_EMPTY + (g & 1)), ((g >> 1) & 1) ^ 1, p.err)))
+              break;
+            issue_s(g, j == n_t - 1);
+          }
+        } else {
+          // P . C(g) once P(g) is written
+          for (int j = 0; ok && j < n_t; ++j) {
+            const int g = g0 + j;
+            if (!(ok = warp_wait(bar(P_FULL + (g & 1)), (g >> 1) & 1, p.err))) break;
+            issue_pv(g, j == 0);
+          }
+        }
+        g0 += n_t;
+        ++seg_i;
+      }
+      // every MMA issued by this thread has completed before TMEM is freed
+      const int fin = s_issuer ? MMA_FINAL : MMA_FINAL_PV;
+      if (lane == 0) {
+        umma_commit_pair(bar(fin), 1);
+        mbar_wait(bar(fin), 0, p.err, MLA_DEVFLAG_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kWarpSoftmax0) {
+    // ------------------------------------------------------------ softmax
+    // Two groups of four warps take alternate tiles (group = g & 1, which is
+    // also the tile's S buffer and P ring slot); warp q of a group reads TMEM
+    // lanes [32q, 32q + 32) for all 64 tokens, so a row's tile maximum needs
+    // no exchange between warps.  The running maximum after tile g is
+    // published per row in shared memory (slot g & 1); a group decides tile
+    // g from the maximum after tile g - 1, which the other group published.
+    const int sw_warp = warp - kWarpSoftmax0;       // 0..7
+    const int grp = sw_warp >> 2;                   // softmax group; also the O block it drains
+    const int gw = sw_warp & 3;                     // warp within the group
+    const int qd = warp & 3;                        // TMEM lanes [32 qd, 32 qd + 32)
+    const int jh = lane >> 4;                       // S row half: partial over CTA jh's columns
+    const int hS = 16 * qd + (lane & 15);           // row (of this CTA's 64) of this thread's S lane
+    const int hO = (32 * qd + lane) & 63;           // row of this thread's O lane
+    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    const uint32_t sw64 = static_cast<uint32_t>((hS >> 1) & 3);  // 64-byte swizzle of row hS
+    float* mx_pub = reinterpret_cast<float*>(base + kOffMax);  // [tile parity][row]
+    float* sums = reinterpret_cast<float*>(base + kOffSum);    // [kind][group][row]
+    const float c_log2 = p.scale_log2;
+    uint32_t grp_phase = 0;
+    // A failed wait (a broken protocol) sets the device flag; the warp then
+    // skips its later waits but still runs every step, so that the group's
+    // named barriers and the other roles' waits stay matched and the kernel
+    // ends.
+    auto rendezvous = [&](bool live) -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GRP));
+      const uint32_t ph = (grp_phase++) & 1;
+      return live && warp_wait(bar(GRP), ph, p.err);
+    };
+
+    TreeWalk walk;
+    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    TreeSegment sg;
+    int g = 0;
+    bool ok = true;
+    while (walk.next(sg)) {
+      const int n = sg.seq.n, P0 = sg.seq.L - n;  // P0: position of the first drafted token
+      // the drafted tokens that this thread's row sees (none for rows past
+      // the block's last, whose results are not written)
+      const int row_s = 64 * (int)rank + hS;
+      unsigned long long seen = 0;
+      if (row_s < sg.rows) {
+        seen = p.mask[sg.seq.row0 + (sg.g * kTreeRows + row_s) / p.n_h];
+        if (n < 64) seen &= (1ull << n) - 1;
+      }
+      const int n_t = sg.t1 - sg.t0;
+      const int g0 = g;
+      // this group's sums over its own tiles of the segment, in the scale of
+      // m_used (the maximum it last applied)
+      float m_used = -INFINITY, l = 0.f, l_exact = 0.f;
+      for (int jt = (grp - g0) & 1; jt < n_t; jt += 2) {
+        const int gt = g0 + jt;
+        const int t = sg.t0 + jt;
+        // ---- partial scores of tile gt -> registers; free the S buffer
+        ok = ok && warp_wait(bar(S_FULL + grp), (gt >> 1) & 1, p.err);
+        tc_fence_after();
+        // sc[16 c + k]: token 32 c + 16 jh + k of the tile, for row hS.
+        // S = partial(CTA 0 columns) + partial(CTA 1 columns): lane jh keeps
+        // tokens [16 jh, 16 jh + 16) of each 32 and hands the rest to lane ^ 16
+        float sc[32];
+        const uint32_t sb = tmem + lane_base + kTmemS + grp * 128;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float va[32], vb[32];
+          tmem_ld32(sb + 32 * c, va);
+          tmem_ld32(sb + 64 + 32 * c, vb);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float own_lo = jh ? vb[k] : va[k], own_hi = jh ? vb[16 + k] : va[16 + k];
+            const float send = jh ? own_lo : own_hi;
+            const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
+            sc[16 * c + k] = (jh ? own_hi : own_lo) + recv;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) signal_lead(S_EMPTY + grp, gw == 0, 16u, gw);
+        const int tok0 = t * kTreeTile;
+        uint32_t clear_lo = 0, clear_hi = 0;  // tokens whose non-finite values must not meet P . C
+        if (tok0 + kTreeTile > P0) {
+          // the tile reaches into the drafted tokens: bit k = position tok0 + k
+          const int sh = tok0 - P0;  // > -64; at most n - 1
+          const unsigned long long vis = sh >= 0 ? seen >> sh : (seen << -sh) | ((1ull << -sh) - 1);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t bits = static_cast<uint32_t>(vis >> (32 * c + 16 * jh));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              // (rows past the sequence's end are zero: their scores are finite)
+              if (!(fabsf(sc[16 * c + k]) <= 3.402823466e38f)) bad |= 1u << (16 * c + k);
+              if (!((bits >> k) & 1u)) sc[16 * c + k] = -INFINITY;
+            }
+          }
+          if (gw == 0 && __any_sync(0xffffffffu, bad != 0)) {
+            clear_lo = __reduce_or_sync(0xffffffffu, (bad & 0xffffu) << (16 * jh));
+            clear_hi = __reduce_or_sync(0xffffffffu, (bad >> 16) << (16 * jh));
+          }
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          mx0 = fmaxf(mx0, sc[k]);
+          mx1 = fmaxf(mx1, sc[k + 1]);
+        }
+        float mx = fmaxf(mx0, mx1);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        // ---- the maximum after this tile.  The running maximum may go
+        // stale: it moves only when a tile's maximum exceeds it by more than
+        // 2^kRescaleThreshold (weights stay below that factor), which keeps O
+        // rescales rare.  Raw scores: scale > 0 commutes with max.
+        const float t_s = mx * c_log2;
+        float m_prev = -INFINITY;
+        if (jt > 0) {  // tile gt - 1 (the other group's) is in this segment
+          ok = ok && warp_wait(bar(DEC + (grp ^ 1)), ((gt - 1) >> 1) & 1, p.err);
+          m_prev = mx_pub[((gt - 1) & 1) * 64 + hS];
+        }
+        const float m_new = (m_prev == -INFINITY || t_s > m_prev + kRescaleThreshold)
+                                ? fmaxf(m_prev, t_s) : m_prev;
+        if (jh == 0) mx_pub[(gt & 1) * 64 + hS] = m_new;
+        named_bar_sync(1 + grp, 128);
+        // O lane hO: rescale if its row's maximum moved at this tile
+        float alpha_o = 1.f;
+        bool resc_o = false;
+        if (jt > 0) {
+          const float mo_prev = mx_pub[((gt - 1) & 1) * 64 + hO];
+          const float mo_new = mx_pub[(gt & 1) * 64 + hO];
+          if (mo_new != mo_prev) {
+            alpha_o = ex2_approx(mo_prev - mo_new);  // mo_prev = -inf: O holds only zeros
+            resc_o = true;
+          }
+        }
+        // the decision of tile gt is published (and slot (gt - 1) & 1 read)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(DEC + grp));
+        // this group's sums move to the new scale
+        if (m_new != m_used) {
+          const float f = m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
+          l *= f;
+          l_exact *= f;
+          m_used = m_new;
+        }
+        const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+        float r0 = 0.f, r1 = 0.f, e0 = 0.f, e1 = 0.f;
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float a = ex2_approx(fmaf(sc[k], c_log2, neg_m));
+          const float b = ex2_approx(fmaf(sc[k + 1], c_log2, neg_m));
+          const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
+          const float2 pf = __bfloat1622float2(pr);
+          if (k & 2) { r1 += pf.x + pf.y; e1 += a + b; } else { r0 += pf.x + pf.y; e0 += a + b; }
+          pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        // u is normalised by the sum of the rounded weights it was built
+        // from; lse uses the unrounded weights
+        l += r0 + r1;
+        l_exact += e0 + e1;
+
+        // P's ring slot grp was last read by PV(gt - 2); O may be rescaled
+        // only after PV(gt - 1) (tiles of an earlier segment were retired by
+        // that segment's epilogue, and the first P . C of a segment
+        // overwrites O)
+        if (gt >= 2) ok = ok && warp_wait(bar(PV_DONE + grp), ((gt - 2) >> 1) & 1, p.err);
+        if (__any_sync(0xffffffffu, resc_o)) {
+          ok = ok && warp_wait(bar(PV_DONE + (grp ^ 1)), ((gt - 1) >> 1) & 1, p.err);
+          tc_fence_after();
+          for (int c0 = 0; c0 < 256; c0 += 32) {  // both O blocks of these lanes
+            float o[32];
+            tmem_ld32(tmem + lane_base + kTmemO + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha_o;
+            tmem_st32(tmem + lane_base + kTmemO + c0, o);
+          }
+          tmem_wait_st();
+        }
+        // P row hS, tokens [32c + 16jh, +16): half c of the row (32 tokens =
+        // 64 B, 64-byte swizzle) lives in the stage's RoPE block (c = 0) or
+        // in ring slot grp (c = 1); 16-byte chunks 2jh and 2jh + 1
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t prow =
+              (c == 0 ? sbase + kOffKv + (gt % kStages) * kStageBytes + 4 * kKvBlk
+                      : sbase + kOffP + grp * kPHalf) + hS * 64;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t ch = static_cast<uint32_t>(2 * jh + k);
+            st_shared_v4(prow + ((ch ^ sw64) << 4), pk[8 * c + 4 * k], pk[8 * c + 4 * k + 1],
+                         pk[8 * c + 4 * k + 2], pk[8 * c + 4 * k + 3]);
+          }
+        }
+        if (clear_lo | clear_hi) {
+          // (uniform in the warp) S of this tile is done, its P . C waits for
+          // this warp: clear the non-finite latent values of those tokens in
+          // this CTA's columns, 16 bytes per lane and token
+          unsigned long long todo = clear_lo | (static_cast<unsigned long long>(clear_hi) << 32);
+          uint8_t* tile = base + kOffKv + (gt % kStages) * kStageBytes + (lane >> 3) * kKvBlk + (lane & 7) * 16;
+          while (todo) {
+            const int k = __ffsll(todo) - 1;
+            todo &= todo - 1;
+            uint4 v = *reinterpret_cast<uint4*>(tile + k * 128);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+            }
+            *reinterpret_cast<uint4*>(tile + k * 128) = v;
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) signal_lead(P_FULL + grp, gw == 0, 16u, gw);
+      }
+      g = g0 + n_t;
+
+      // ---- epilogue: u = O / l for this thread's O lane (one row, 128
+      // consecutive latent columns of O block grp)
+      // the maximum after the segment's last tile (decided by either group)
+      if (((g - 1) & 1) != grp) ok = ok && warp_wait(bar(DEC + (grp ^ 1)), ((g - 1) >> 1) & 1, p.err);
+      const float mS_fin = mx_pub[((g - 1) & 1) * 64 + hS];
+      const float mO_fin = mx_pub[((g - 1) & 1) * 64 + hO];
+      {
+        // this group's sums in the scale of the final maximum
+        const float f = m_used == mS_fin ? 1.f : m_used == -INFINITY ? 0.f : ex2_approx(m_used - mS_fin);
+        const float lf = l * f, lef = l_exact * f;
+        const float l2 = lf + __shfl_xor_sync(0xffffffffu, lf, 16);
+        const float e2 = lef + __shfl_xor_sync(0xffffffffu, lef, 16);
+        if (jh == 0) {
+          sums[(0 * 2 + grp) * 64 + hS] = l2;
+          sums[(1 * 2 + grp) * 64 + hS] = e2;
+        }
+      }
+      // every warp has read the published maxima of this segment before any
+      // starts the next one
+      ok = rendezvous(ok);
+      const float l_o = sums[(0 * 2 + 0) * 64 + hO] + sums[(0 * 2 + 1) * 64 + hO];
+      const float le_o = sums[(1 * 2 + 0) * 64 + hO] + sums[(1 * 2 + 1) * 64 + hO];
+      ok = ok && warp_wait(bar(PV_DONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.err);
+      tc_fence_after();
+      // no token seen: u = 0 (a NaN sum, of non-finite scores, stays)
+      const float inv = l_o == 0.f ? 0.f : 1.f / l_o;
+      const int c = grp;                          // O block drained by this group
+      const int col0 = 256 * c + 128 * (qd >> 1);  // latent column of TMEM column kTmemO + 128c
+      // The segment's last S has read Q, so the query area stages the output:
+      // 8 KB per warp, its 32 rows x 128 columns as boxes of 128-byte lines
+      // (64 bf16 or 32 fp32 columns) in the 128-byte-swizzled layout of the
+      // output tensor map (16-byte chunk k of row r at k ^ (r & 7)).
+      const uint32_t stg = sbase + kOffQ + sw_warp * 8192u;
+      const int y_w = 64 * (int)rank + 32 * (qd & 1);  // this warp's first row of the block
+      const int y_out = sg.whole ? sg.first + y_w : sg.slot * kTreeRows + y_w;
+      const bool full = !sg.whole || y_w + 32 <= sg.rows;
+      if (y_w >= sg.rows) {
+        // none of this warp's rows exist
+      } else if (full && (p.out_f32 || !sg.whole)) {
+        const CUtensorMap* omap = sg.whole ? &p.maps.u_out : &p.maps.part_out;
+        // fp32: four boxes of 32 columns, two at a time through the 8 KB
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float o[32];
+          tmem_ld32(tmem + lane_base + kTmemO + c * 128 + c0, o);
+          tmem_wait_ld();
+          const uint32_t box = stg + static_cast<uint32_t>((c0 >> 5) & 1) * 4096u;
+          if (c0 == 64) {  // the first two boxes must have left before reuse
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            st_shared_v4(box + lane * 128u + ((static_cast<uint32_t>(e ^ (lane & 7))) << 4),
+                         __float_as_uint(o[4 * e] * inv), __float_as_uint(o[4 * e + 1] * inv),
+                         __float_as_uint(o[4 * e + 2] * inv), __float_as_uint(o[4 * e + 3] * inv));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(omap, box, col0 + c0, y_out);
+            bulk_commit();
+          }
+        }
+      } else {
+        const bool live = y_w + lane < sg.rows;
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float o[32];
+          tmem_ld32(tmem + lane_base + kTmemO + c * 128 + c0, o);
+          tmem_wait_ld();
+          const size_t at = ((size_t)y_out + lane) * kDc + col0 + c0;
+          if (p.out_f32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.u) + at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (live)
+                dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+            continue;
+          }
+          const uint32_t row = stg + static_cast<uint32_t>(c0 >> 6) * 4096u + lane * 128u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * e + 2 * k] * inv, o[8 * e + 2 * k + 1] * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            if (full) {
+              const uint32_t chunk16 = static_cast<uint32_t>(((c0 & 63) >> 3) + e);
+              st_shared_v4(row + ((chunk16 ^ static_cast<uint32_t>(lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            } else if (live) {
+              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + at)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (full && (c0 & 32)) {  // box c0 >> 6 is complete
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&p.maps.u_out, stg + static_cast<uint32_t>(c0 >> 6) * 4096u, col0 + (c0 & 64), y_out);
+              bulk_commit();
+            }
+          }
+        }
+      }
+      if (y_w + lane < sg.rows && qd < 2 && c == 0) {
+        const float lse = le_o == 0.f ? -INFINITY : (mO_fin + log2f(le_o)) * 0.69314718055994531f;
+        if (!sg.whole)
+          p.part_lse[y_out + lane] = lse;
+        else if (p.lse != nullptr)
+          p.lse[y_out + lane] = lse;
+      }
+      // the query area may take the next segment's rows once the stores have
+      // read it
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(EPI_FREE));
+      tc_fence_before();
+    }
+    // the last stores complete before the CTA exits
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // all paired MMAs are complete and no arrival is still on its way
+  if (warp == kWarpAlloc) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+  cluster_sync();
+}
+
+}  // namespace
+
+// Per device, once: opt in to the shared-memory size and count how many
+// 2-CTA clusters of this kernel can be resident at the same time.
+int tree_sm100_prepare() {
+  if (cudaFuncSetAttribute(tree_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmemBytes) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, tree_sm100_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+cudaError_t launch_tree_sm100(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s) {
+  Params p;
+  p.maps = maps;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kv = static_cast<const __nv_bfloat16*>(a.kv);
+  p.block_table = a.block_table;
+  p.seqlens = a.seqlens;
+  p.cu_q = a.cu_q;
+  p.mask = a.mask;
+  p.rec = a.rec;
+  p.part_lse = a.part_lse;
+  p.u = a.u;
+  p.lse = a.lse;
+  p.err = a.err;
+  p.B = a.B;
+  p.T = a.T;
+  p.n_h = a.n_h;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.num_pages = a.num_pages;
+  p.out_f32 = a.out_f32 ? 1 : 0;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * a.num_chunks, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_sm100_kernel, p);
+}
+
+}  // namespace mla

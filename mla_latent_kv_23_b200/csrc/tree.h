@@ -1,0 +1,71 @@
+// Declarations shared by the kernels of the speculative-decoding operators
+// (tree attention, block tables and slot maps, accepted branches).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mla {
+
+constexpr int kTreeTile = 64;      // cache rows per attention tile
+constexpr int kTreeMaxNodes = 64;  // drafted tokens of one sequence: the bits of a mask word
+constexpr int kTreeRows = 128;     // (token, head) rows of one row block
+
+// Cost of one more segment inside a KV chunk (the next rows' queries, the
+// output of the last), in 64-token tiles.
+constexpr int kTreeSegTiles = 6;
+
+// Workspace of mla_decode_tree.  rec: 4 ints per chunk boundary (G + 1 of
+// them): sequence, row block and tile where the chunk starts, 0; the last one
+// is (B, 0, 0, 0).  up / cp: per-sequence prefix sums of the plan, used there
+// only when the batch is too large for shared memory.  part_u / part_lse: the
+// partial results of pieces of row blocks, 128 rows per slot: chunk c writes a
+// piece that continues a block into slot 2c and one that begins a block in
+// slot 2c + 1 (fp32).
+struct TreeWsLayout {
+  size_t rec = 0, up = 0, cp = 0, part_lse = 0, part_u = 0, total = 0;
+};
+TreeWsLayout tree_ws_layout(int B, int d_c, int num_chunks);
+
+struct TreeArgs {
+  const void* q;
+  const void* kv;
+  const int* block_table;
+  const int* seqlens;
+  const int* cu_q;
+  const unsigned long long* mask;
+  void* u;
+  float* lse;
+  int* rec;
+  long long* up;
+  int* cp;
+  float* part_u;
+  float* part_lse;
+  int* err;
+  int B, T, n_h, d_c, d_R, page_size, max_pages, num_pages, num_chunks;
+  float scale;
+  bool bf16;     // q and the cache (else fp32)
+  bool out_f32;  // u
+};
+
+cudaError_t launch_tree_plan(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
+
+// The DeepSeek-V3-shape attend kernel: bf16, d_c = 512, d_R = 64.  The rows of
+// q [T, n_h, 576] and u [T, n_h, 512] are flat: row t n_h + h.
+//   kv_lat4 / kv_rope: one CTA's latent blocks of 64 cache rows in one copy,
+//     and its RoPE block;
+//   q_lat4 / q_rope4 (n_h a multiple of 16, has_q4): a CTA's 64 rows, both
+//     column halves, in one copy per 64-column block;
+//   q_lat / q_rope: 16 rows of one column half;
+//   u_out: 32 rows of u, 128 bytes of columns; part_out the same of part_u.
+struct TreeMaps {
+  CUtensorMap kv_lat4, kv_rope, q_lat4, q_rope4, q_lat, q_rope, u_out, part_out;
+  int has_q4;
+};
+int tree_sm100_prepare();  // co-resident clusters, 0 if the kernel cannot run
+cudaError_t launch_tree_sm100(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);
+
+}  // namespace mla

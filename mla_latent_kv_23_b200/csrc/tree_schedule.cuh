@@ -1,0 +1,123 @@
+// Work of the tree attention: row blocks, chunks and segments.
+//
+// A sequence with n drafted tokens and n_h heads has n n_h query rows (flat
+// row i = token i / n_h, head i % n_h), all against the same cached tokens.
+// They are taken in blocks of 128 rows, the M dimension of the contractions:
+// one block per token at 128 heads, eight tokens per block at 16 heads.  A
+// block crosses every 64-token tile of its sequence; a chunk is a run of
+// (sequence, block, tile) in that order, given by where it and the next chunk
+// start, and the part of a chunk inside one block is a segment.  A segment
+// that covers a whole block writes u and lse, any other a partial result.
+#pragma once
+
+#include "mla.h"
+#include "tree.h"
+
+namespace mla {
+
+// Sequence b as the kernels see it.  n = 0 where it has no drafted tokens, or
+// where what the host cannot see is wrong (flag != 0): nothing is read or
+// written out of range for it.
+struct TreeSeq {
+  int row0;    // its first token of the packed rows
+  int n;       // drafted tokens, the last n of its L cached ones
+  int L;
+  int blocks;  // row blocks
+  int tiles;
+  int flag;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const int* __restrict__ cu_q,
+                                            const int* __restrict__ seqlens, int b, int T, int n_h,
+                                            long long max_len) {
+  TreeSeq s;
+  s.row0 = cu_q[b];
+  const int end = cu_q[b + 1];
+  s.L = seqlens[b];
+  s.n = 0;
+  s.flag = 0;
+  // (with cu_q[b - 1] > cu_q[b] the rows may be the sequence's before it, too)
+  if (s.row0 < 0 || end < s.row0 || end > T || end - s.row0 > kTreeMaxNodes ||
+      (b > 0 && cu_q[b - 1] > s.row0))
+    s.flag = MLA_DEVFLAG_BAD_TREE;
+  else
+    s.n = end - s.row0;
+  s.blocks = s.tiles = 0;
+  if (s.n > 0) {
+    if (s.L < s.n || s.L > max_len) {
+      s.flag = MLA_DEVFLAG_BAD_SEQLEN;  // its rows get u = 0, lse = -inf
+    } else {
+      s.blocks = (s.n * n_h + kTreeRows - 1) / kTreeRows;
+      s.tiles = (s.L - 1) / kTreeTile + 1;
+    }
+  }
+  return s;
+}
+
+struct TreeSegment {
+  int b, g;    // sequence, row block
+  int t0, t1;  // tiles
+  int whole;   // covers every tile of the block
+  int slot;    // partial slot where it does not
+  int first;   // the block's first flat row
+  int rows;    // the block's rows (<= 128)
+  TreeSeq seq;
+};
+
+struct TreeWalk {
+  const int *cu_q, *seqlens;
+  int B, T, n_h, chunk;
+  long long max_len;
+  int b, g, t;     // next tile
+  int be, ge, te;  // where the next chunk starts
+  bool loaded;
+  TreeSeq seq;
+
+  __device__ __forceinline__ void init(const int* rec, const int* cu, const int* lens, int nseq,
+                                       int rows, int heads, long long longest, int chunk_id) {
+    cu_q = cu;
+    seqlens = lens;
+    B = nseq;
+    T = rows;
+    n_h = heads;
+    max_len = longest;
+    chunk = chunk_id;
+    const int4 r0 = *reinterpret_cast<const int4*>(rec + 4 * chunk_id);
+    const int4 r1 = *reinterpret_cast<const int4*>(rec + 4 * chunk_id + 4);
+    b = r0.x;
+    g = r0.y;
+    t = r0.z;
+    be = r1.x;
+    ge = r1.y;
+    te = r1.z;
+    loaded = false;
+  }
+
+  __device__ __forceinline__ bool next(TreeSegment& s) {
+    while (true) {
+      if (b >= B || b > be || (b == be && (g > ge || (g == ge && t >= te)))) return false;
+      if (!loaded) {
+        seq = tree_seq(cu_q, seqlens, b, T, n_h, max_len);
+        loaded = true;
+      }
+      if (g < seq.blocks) break;
+      ++b;
+      g = t = 0;
+      loaded = false;
+    }
+    s.b = b;
+    s.g = g;
+    s.t0 = t;
+    s.t1 = (b == be && g == ge) ? min(te, seq.tiles) : seq.tiles;
+    s.whole = t == 0 && s.t1 == seq.tiles;
+    s.slot = 2 * chunk + (t == 0 ? 1 : 0);
+    s.first = seq.row0 * n_h + g * kTreeRows;
+    s.rows = min(kTreeRows, seq.n * n_h - g * kTreeRows);
+    s.seq = seq;
+    ++g;
+    t = 0;
+    return true;
+  }
+};
+
+}  // namespace mla

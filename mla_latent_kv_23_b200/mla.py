@@ -20,6 +20,7 @@ MLA_DTYPE_FP32 = 1
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_CUDA",
           4: "MLA_ERR_WORKSPACE_TOO_SMALL", 5: "MLA_ERR_DEVICE_CHECK"}
 DEVFLAG_BAD_SEQLEN, DEVFLAG_BAD_PAGE, DEVFLAG_TIMEOUT, DEVFLAG_LAYOUT, DEVFLAG_RANGE = 1, 2, 4, 8, 16
+DEVFLAG_BAD_TREE, DEVFLAG_NO_PAGES, DEVFLAG_NO_ROOM = 0x20, 0x40, 0x80
 
 
 class MLAError(RuntimeError):
@@ -52,6 +53,35 @@ class GqaParams(ctypes.Structure):
                 ("num_splits", ctypes.c_int), ("o_fp32", ctypes.c_int)]
 
 
+class TreeParams(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("kv_cache", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seqlens", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+                ("u", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("T", ctypes.c_int), ("n_h", ctypes.c_int),
+                ("d_c", ctypes.c_int), ("d_R", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("softmax_scale", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("num_splits", ctypes.c_int), ("u_fp32", ctypes.c_int)]
+
+
+class TablesParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("ctx_lens", "new_lens", "pages_held", "block_table", "free_pages", "free_used",
+                 "free_used_out", "seqlens", "cu_new", "pages_held_out", "seq_ids", "pos", "slots",
+                 "parents", "tree_mask")] + \
+               [(n, ctypes.c_int) for n in
+                ("B", "max_pages_per_seq", "n_free", "max_tokens", "page_size", "num_pages")]
+
+
+class AcceptParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("kv_cache", "block_table", "seqlens", "cu_q", "tree_mask", "accepted",
+                 "seqlens_out", "path")] + \
+               [(n, ctypes.c_int) for n in
+                ("B", "T", "width", "page_size", "max_pages_per_seq", "num_pages", "dtype")]
+
+
 _V, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _P = ctypes.POINTER(DecodeParams)
 _PG = ctypes.POINTER(GqaParams)
@@ -77,6 +107,11 @@ SIGNATURES = {
     "mla_decode_gqa": ([_PG, _V, _S, _V], _I),
     "mla_up_proj": ([_V, _V, _V, _I, _I, _I, _I, _I, _I, _V], _I),
     "mla_merge_partials": ([_V, _V, _V, _V, _I, _I, _I, _I, _V], _I),
+    "mla_append_latent_slots": ([_V, _V, _V, _V, _V, _V, _I, _I, _I, _I, _I, _F, _I, _V], _I),
+    "mla_build_tables": ([ctypes.POINTER(TablesParams), _V], _I),
+    "mla_decode_tree_workspace_size": ([ctypes.POINTER(TreeParams), ctypes.POINTER(_S)], _I),
+    "mla_decode_tree": ([ctypes.POINTER(TreeParams), _V, _S, _V], _I),
+    "mla_accept_tree": ([ctypes.POINTER(AcceptParams), _V], _I),
     "mla_check_device_errors": ([_V, ctypes.POINTER(_I)], _I),
     "mla_selftest_wait": ([_I, _V], _I),
 }
@@ -344,6 +379,194 @@ def mla_merge_partials(u_parts, lse_parts, u, lse=None, stream=None) -> None:
                                     d_c, _dtype_code(u), _stream(stream)), "mla_merge_partials")
 
 
+# ----------------------------------------------------------------------------
+# speculative decoding: tables, append, tree attention, accepted branch
+# ----------------------------------------------------------------------------
+def _int_tensor(t, name: str, shape, dtype=None):
+    """t is an int32 (or `dtype`) tensor of the given shape (None: any size)."""
+    torch = _torch()
+    dtype = dtype or torch.int32
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _one_device(*tensors):
+    """The device that all given tensors (None aside) are on."""
+    dev = {t.device for t in tensors if t is not None}
+    if len(dev) != 1 or next(iter(dev)).type != "cuda":
+        raise ValueError("tensors must be on one CUDA device")
+    return dev.pop()
+
+
+class _On:
+    """Makes a device current for a call: the library works on the current
+    one.  A stream handle stays the caller's."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        torch = _torch()
+        self.back = torch.cuda.current_device()
+        if self.back != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.back != self.device.index:
+            _torch().cuda.set_device(self.back)
+
+
+def _keep(p, device, *tensors):
+    """The parameters hold raw pointers: keep what they point to, and the
+    device that the call has to be made on."""
+    p.device = device
+    p.tensors = tensors
+    return p
+
+
+def mla_append_latent_slots(h, W_DKV, W_KR, slots, pos, kv_cache, rope_base: float = 10000.0,
+                            stream=None) -> None:
+    """kv_cache[slots[t]] = [W_DKV h[t] || RoPE(W_KR h[t], pos[t])] for every
+    token with slots[t] >= 0 (see include/mla.h)."""
+    T, d_model = h.shape
+    d_c, d_R = W_DKV.shape[0], W_KR.shape[0]
+    rows, width = kv_cache.shape
+    if W_DKV.shape[1] != d_model or W_KR.shape[1] != d_model or width != d_c + d_R:
+        raise ValueError("W_DKV [d_c, d_model], W_KR [d_R, d_model], kv_cache [rows, d_c + d_R] expected")
+    if not h.dtype == W_DKV.dtype == W_KR.dtype == kv_cache.dtype:
+        raise TypeError("h, W_DKV, W_KR and kv_cache must have one dtype")
+    _int_tensor(slots, "slots", (T,))
+    _int_tensor(pos, "pos", (T,))
+    if T == 0:
+        return
+    with _On(_one_device(h, W_DKV, W_KR, slots, pos, kv_cache)):
+        _check(lib().mla_append_latent_slots(_ptr(h), _ptr(W_DKV), _ptr(W_KR), _ptr(slots), _ptr(pos),
+                                             _ptr(kv_cache), rows, T, d_model, d_c, d_R,
+                                             float(rope_base), _dtype_code(h), _stream(stream)),
+               "mla_append_latent_slots")
+
+
+def tables_params(ctx_lens, new_lens, block_table, free_pages, free_used, free_used_out, seqlens,
+                  cu_new, seq_ids, pos, slots, page_size: int, num_pages: int, parents=None,
+                  tree_mask=None, pages_held=None, pages_held_out=None) -> TablesParams:
+    """Pack mla_tables_params: lengths [B], block_table [B, max_pages],
+    free_pages [F], free_used and free_used_out [1], cu_new [B + 1]; seq_ids,
+    pos, slots, and for drafted trees parents (int32) and tree_mask (int64),
+    [max_tokens]."""
+    torch = _torch()
+    B = ctx_lens.shape[0]
+    n = slots.shape[0]
+    _int_tensor(block_table, "block_table", (B, None))
+    for t, name, size in ((ctx_lens, "ctx_lens", B), (new_lens, "new_lens", B), (seqlens, "seqlens", B),
+                          (cu_new, "cu_new", B + 1), (free_pages, "free_pages", None),
+                          (free_used, "free_used", 1), (free_used_out, "free_used_out", 1),
+                          (seq_ids, "seq_ids", n), (pos, "pos", n), (slots, "slots", n),
+                          (parents, "parents", n), (pages_held, "pages_held", B),
+                          (pages_held_out, "pages_held_out", B)):
+        if t is not None:
+            _int_tensor(t, name, (size,))
+    if tree_mask is not None:
+        _int_tensor(tree_mask, "tree_mask", (n,), torch.int64)
+    every = (ctx_lens, new_lens, block_table, free_pages, free_used, free_used_out, seqlens, cu_new,
+             seq_ids, pos, slots, parents, tree_mask, pages_held, pages_held_out)
+    p = TablesParams(ctx_lens=_ptr(ctx_lens), new_lens=_ptr(new_lens), pages_held=_ptr(pages_held),
+                     block_table=_ptr(block_table), free_pages=_ptr(free_pages),
+                     free_used=_ptr(free_used), free_used_out=_ptr(free_used_out),
+                     seqlens=_ptr(seqlens), cu_new=_ptr(cu_new), pages_held_out=_ptr(pages_held_out),
+                     seq_ids=_ptr(seq_ids), pos=_ptr(pos), slots=_ptr(slots), parents=_ptr(parents),
+                     tree_mask=_ptr(tree_mask), B=B, max_pages_per_seq=block_table.shape[1],
+                     n_free=free_pages.shape[0], max_tokens=n, page_size=page_size,
+                     num_pages=num_pages)
+    return _keep(p, _one_device(*every), *every)
+
+
+def mla_build_tables(p: TablesParams, stream=None) -> None:
+    """Pages, slots, positions and tree masks of a step's new tokens."""
+    with _On(p.device):
+        _check(lib().mla_build_tables(ctypes.byref(p), _stream(stream)), "mla_build_tables")
+
+
+def tree_params(q, kv_cache, block_table, seqlens, cu_q, tree_mask, u, lse, page_size: int, d_R: int,
+                softmax_scale: float, num_splits: int = 0) -> TreeParams:
+    """Pack mla_tree_params: q [T, n_h, d_c + d_R], kv_cache [rows, d_c + d_R],
+    block_table [B, max_pages], seqlens [B], cu_q [B + 1], tree_mask [T] int64,
+    u [T, n_h, d_c] (the dtype of q, or float32), lse [T, n_h] or None."""
+    torch = _torch()
+    T, n_h, W = q.shape
+    B = seqlens.shape[0]
+    d_c = W - d_R
+    if kv_cache.dtype != q.dtype or (u.dtype != q.dtype and u.dtype != torch.float32):
+        raise TypeError("kv_cache must have the dtype of q, u that or float32")
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != W or kv_cache.shape[0] % page_size != 0:
+        raise ValueError("kv_cache must be [num_pages * page_size, d_c + d_R]")
+    if tuple(u.shape) != (T, n_h, d_c):
+        raise ValueError("u must be [T, n_h, d_c]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, n_h)):
+        raise ValueError("lse must be float32 [T, n_h]")
+    _int_tensor(block_table, "block_table", (B, None))
+    _int_tensor(seqlens, "seqlens", (B,))
+    _int_tensor(cu_q, "cu_q", (B + 1,))
+    _int_tensor(tree_mask, "tree_mask", (T,), torch.int64)
+    every = (q, kv_cache, block_table, seqlens, cu_q, tree_mask, u, lse)
+    p = TreeParams(q=_ptr(q), kv_cache=_ptr(kv_cache), block_table=_ptr(block_table),
+                   seqlens=_ptr(seqlens), cu_q=_ptr(cu_q), tree_mask=_ptr(tree_mask), u=_ptr(u),
+                   lse=_ptr(lse), B=B, T=T, n_h=n_h, d_c=d_c, d_R=d_R, page_size=page_size,
+                   max_pages_per_seq=block_table.shape[1],
+                   num_pages=kv_cache.shape[0] // page_size, softmax_scale=float(softmax_scale),
+                   dtype=_dtype_code(q), num_splits=num_splits,
+                   u_fp32=int(u.dtype == torch.float32))
+    return _keep(p, _one_device(*every), *every)
+
+
+def mla_decode_tree_workspace_size(p: TreeParams) -> int:
+    n = _S(0)
+    with _On(p.device):
+        _check(lib().mla_decode_tree_workspace_size(ctypes.byref(p), ctypes.byref(n)),
+               "mla_decode_tree_workspace_size")
+    return n.value
+
+
+def mla_decode_tree(p: TreeParams, workspace, stream=None) -> None:
+    """Attention of drafted trees over the paged latent cache."""
+    with _On(p.device):
+        _check(lib().mla_decode_tree(ctypes.byref(p), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+               "mla_decode_tree")
+
+
+def accept_params(kv_cache, block_table, seqlens, cu_q, tree_mask, accepted, seqlens_out, path,
+                  page_size: int) -> AcceptParams:
+    """Pack mla_accept_params: kv_cache [rows, d_c + d_R], block_table
+    [B, max_pages], seqlens, accepted and seqlens_out [B] (seqlens_out may be
+    seqlens), cu_q [B + 1], tree_mask (int64) and path [T]."""
+    torch = _torch()
+    B, T = seqlens.shape[0], path.shape[0]
+    if kv_cache.dim() != 2 or kv_cache.shape[0] % page_size != 0:
+        raise ValueError("kv_cache must be [num_pages * page_size, d_c + d_R]")
+    _int_tensor(block_table, "block_table", (B, None))
+    for t, name, size in ((seqlens, "seqlens", B), (cu_q, "cu_q", B + 1), (accepted, "accepted", B),
+                          (seqlens_out, "seqlens_out", B), (path, "path", T)):
+        _int_tensor(t, name, (size,))
+    _int_tensor(tree_mask, "tree_mask", (T,), torch.int64)
+    every = (kv_cache, block_table, seqlens, cu_q, tree_mask, accepted, seqlens_out, path)
+    p = AcceptParams(kv_cache=_ptr(kv_cache), block_table=_ptr(block_table), seqlens=_ptr(seqlens),
+                     cu_q=_ptr(cu_q), tree_mask=_ptr(tree_mask), accepted=_ptr(accepted),
+                     seqlens_out=_ptr(seqlens_out), path=_ptr(path), B=B, T=T,
+                     width=kv_cache.shape[1], page_size=page_size,
+                     max_pages_per_seq=block_table.shape[1],
+                     num_pages=kv_cache.shape[0] // page_size, dtype=_dtype_code(kv_cache))
+    return _keep(p, _one_device(*every), *every)
+
+
+def mla_accept_tree(p: AcceptParams, stream=None) -> None:
+    """The accepted branches' cache rows, moved behind their contexts."""
+    with _On(p.device):
+        _check(lib().mla_accept_tree(ctypes.byref(p), _stream(stream)), "mla_accept_tree")
+
+
 def mla_check_device_errors(stream=None) -> int:
     """Synchronize, then return the device flags (raises MLAError if any is set)."""
     f = _I(0)
@@ -378,6 +601,27 @@ def decode(q, kv_cache, block_table, seqlens, page_size: int, d_R: int, softmax_
                       num_splits)
     ws = torch.empty(max(mla_decode_workspace_size(p), 256), dtype=torch.uint8, device=q.device)
     mla_decode(p, ws, stream)
+    return u, lse
+
+
+def decode_tree(q, kv_cache, block_table, seqlens, cu_q, tree_mask, page_size: int, d_R: int,
+                softmax_scale: float, num_splits: int = 0, with_lse: bool = True, stream=None,
+                u_dtype=None):
+    """Returns (u [T, n_h, d_c], lse [T, n_h] or None) of the drafted tokens'
+    rows q [T, n_h, d_c + d_R]; rows past cu_q[B] are zero.  With a `stream`
+    the results and the workspace belong to that stream."""
+    torch = _torch()
+    T, n_h, W = q.shape
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=q.device)
+    with torch.cuda.stream(stream):
+        u = torch.zeros((T, n_h, W - d_R), dtype=u_dtype or torch.float32, device=q.device)
+        lse = torch.zeros((T, n_h), dtype=torch.float32, device=q.device) if with_lse else None
+        p = tree_params(q, kv_cache, block_table, seqlens, cu_q, tree_mask, u, lse, page_size, d_R,
+                        softmax_scale, num_splits)
+        ws = torch.empty(max(mla_decode_tree_workspace_size(p), 256), dtype=torch.uint8,
+                         device=q.device)
+        mla_decode_tree(p, ws)
     return u, lse
 
 
