@@ -77,8 +77,6 @@ mla_status encode_tree(TreeMaps* m, const mla_tree_params* p, const TreeArgs& a)
     ok &= encode(&m->kv_rope, kBf16, 2, p->kv_cache, dims, strides, box, k64);
   }
   m->has_q4 = p->n_h % 16 == 0;
-  memset(&m->q_lat4, 0, sizeof(m->q_lat4));
-  memset(&m->q_rope4, 0, sizeof(m->q_rope4));
   if (m->has_q4) {  // (column, row within 16, column half, 16 rows)
     const cuuint64_t dims[4] = {384, 16, 2, rows / 16}, strides[3] = {kRow, 256, 16 * kRow};
     const cuuint32_t box[4] = {64, 16, 2, 4};
@@ -86,8 +84,7 @@ mla_status encode_tree(TreeMaps* m, const mla_tree_params* p, const TreeArgs& a)
     const cuuint64_t rdims[4] = {544, 16, 2, rows / 16}, rstrides[3] = {kRow, 64, 16 * kRow};
     const cuuint32_t rbox[4] = {32, 16, 2, 4};
     ok &= encode(&m->q_rope4, kBf16, 4, p->q, rdims, rstrides, rbox, k64);
-  }
-  {
+  } else {
     const cuuint64_t dims[2] = {576, rows}, strides[1] = {kRow};
     const cuuint32_t box[2] = {64, 16}, rbox[2] = {32, 16};
     ok &= encode(&m->q_lat, kBf16, 2, p->q, dims, strides, box, k128);
@@ -237,6 +234,9 @@ mla_status mla_build_tables(const mla_tables_params* p, void* stream) {
   a.max_tokens = p->max_tokens;
   a.page_size = p->page_size;
   a.num_pages = p->num_pages;
+  a.page_shift = -1;
+  if ((p->page_size & (p->page_size - 1)) == 0)
+    for (a.page_shift = 0; (1 << a.page_shift) < p->page_size;) ++a.page_shift;
   return cuda_status(launch_build_tables(a, d->sm_count, static_cast<cudaStream_t>(stream)));
 }
 

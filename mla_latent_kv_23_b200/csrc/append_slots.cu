@@ -71,14 +71,16 @@ __device__ __forceinline__ float2 rope_pair(float x0, float x1, int pos, double 
   return make_float2(x0 * c - x1 * s, x0 * s + x1 * c);
 }
 
-// Grid (cluster, token blocks, feature tiles), cluster (cs, 1, 1) along K.
+// Grid (kCs, token blocks, feature tiles), cluster (kCs, 1, 1) along K.
+template <int kCs>
 __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x, cs = gridDim.x;
+  constexpr int cs = kCs;
+  const int rank = blockIdx.x;
   const int t0 = blockIdx.y * p.n_blk;
   const bool rope = (int)blockIdx.z >= p.tiles0;
   const int row0 = ((int)blockIdx.z - (rope ? p.tiles0 : 0)) * 128;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar(FULL + s), 1);
+      mbar_init(bar(FULL + s), 2);  // the two producers
       mbar_init(bar(EMPTY + s), 1);
     }
     mbar_init(bar(DONE), 1);
@@ -104,15 +106,26 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kOffSlot);
 
+  // this warp's tokens of the epilogue, one per lane: token `lane` of them is
+  // (warp + kWarps lane) cs + rank of the block
+  const int nt = min(p.n_blk, p.T - t0);
+  const int my_t = (warp + kWarps * lane) * cs + rank;
+  const int my_slot = my_t < nt ? p.slots[t0 + my_t] : -1;
+  const int my_pos = my_t < nt && rope ? p.pos[t0 + my_t] : 0;
+
   bool ok = true;
-  if (warp == 0 && lane == 0) {
-    const CUtensorMap* wm = &p.w_map[rope ? 1 : 0];
+  if ((warp == 0 || warp == 2) && lane == 0) {
+    // producers: warp 0 the weights, warp 2 the tokens
+    const CUtensorMap* m = warp == 2 ? &p.x_map : &p.w_map[rope ? 1 : 0];
+    const uint32_t bytes = warp == 2 ? xblk : kWBlk, off = warp == 2 ? kWBlk : 0;
+    const int y = warp == 2 ? t0 : row0;
     for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
       const int s = i % p.stages;
-      if (!(ok = mbar_wait(bar(EMPTY + s), ((i / p.stages) & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT))) break;
-      mbar_arrive_expect_tx(bar(FULL + s), stage);
-      tma_load_2d(sbase + s * stage, wm, bar(FULL + s), kb * 64, row0);
-      tma_load_2d(sbase + s * stage + kWBlk, &p.x_map, bar(FULL + s), kb * 64, t0);
+      if (i >= p.stages &&
+          !(ok = mbar_wait(bar(EMPTY + s), ((i / p.stages) & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT)))
+        break;
+      mbar_arrive_expect_tx(bar(FULL + s), bytes);
+      tma_load_2d(sbase + s * stage + off, m, bar(FULL + s), kb * 64, y);
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_bf16(128, p.n_blk, false);
@@ -155,26 +168,29 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
   const bool live = ok && f < (rope ? p.d_R : p.d_c);
   const double freq0 = rope ? exp(-(double)f / (double)p.d_R * p.log_base) : 0.0;
   const double freq1 = rope ? exp(-(double)(f + 2) / (double)p.d_R * p.log_base) : 0.0;
-  const int nt = min(p.n_blk, p.T - t0);
-  for (int t = warp * cs + rank; t < nt; t += kWarps * cs) {
-    const int slot = p.slots[t0 + t];
+  for (int k = 0; k < (kMaxTokens + kWarps * cs - 1) / (kWarps * cs); ++k) {
+    const int t = (warp + kWarps * k) * cs + rank;
+    if (t >= nt) break;
+    const int slot = __shfl_sync(0xffffffffu, my_slot, k), pos = __shfl_sync(0xffffffffu, my_pos, k);
     if (slot < 0) continue;
     if (slot >= p.rows) {
       if (lane == 0) atomicOr(p.err, MLA_DEVFLAG_BAD_PAGE);
       continue;
     }
     const uint32_t at = sbase + (t * 128 + 4 * lane) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < cs; ++r) {
-      const float4 y = ld_cluster_v4(mapa(at, r));
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
+    float4 y[cs];
+#pragma unroll
+    for (int r = 0; r < cs; ++r) y[r] = ld_cluster_v4(mapa(at, r));
+    float4 x = y[0];
+#pragma unroll
+    for (int r = 1; r < cs; ++r) {
+      x.x += y[r].x;
+      x.y += y[r].y;
+      x.z += y[r].z;
+      x.w += y[r].w;
     }
     if (!live) continue;
     if (rope) {
-      const int pos = p.pos[t0 + t];
       const float2 a = rope_pair(x.x, x.y, pos, freq0), b = rope_pair(x.z, x.w, pos, freq1);
       x = make_float4(a.x, a.y, b.x, b.y);
     }
@@ -235,8 +251,11 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 int append_slots_prepare() {
-  if (cudaFuncSetAttribute(append_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kSmem) != cudaSuccess) {
+  auto prepare = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) == cudaSuccess;
+  };
+  if (!prepare(append_slots_kernel<1>) || !prepare(append_slots_kernel<2>) ||
+      !prepare(append_slots_kernel<4>) || !prepare(append_slots_kernel<8>)) {
     cudaGetLastError();
     return 0;
   }
@@ -273,8 +292,11 @@ cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_d
   p.log_base = log(a.rope_base);
   const int tiles = p.tiles0 + (a.d_R > 0 ? (a.d_R + 127) / 128 : 0);
   const int blocks = (a.T + p.n_blk - 1) / p.n_blk;
-  // K over as many CTAs as fill the SMs once, each with 4 blocks of 64 or more
-  const int cs = std::max(1, std::min({kMaxCluster, a.sm_count / (tiles * blocks), a.d_model / 256}));
+  // K over as many CTAs as fill the SMs once (powers of two: a cluster sits in
+  // one GPC, and others would leave SMs of it idle), each with 4 blocks of 64
+  // columns or more
+  int cs = 1;
+  while (2 * cs <= kMaxCluster && 2 * cs * tiles * blocks <= a.sm_count && 2 * cs * 256 <= a.d_model) cs *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs, blocks, tiles);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -287,7 +309,10 @@ cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_d
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_slots_kernel, p);
+  return cs == 8   ? cudaLaunchKernelEx(&cfg, append_slots_kernel<8>, p)
+         : cs == 4 ? cudaLaunchKernelEx(&cfg, append_slots_kernel<4>, p)
+         : cs == 2 ? cudaLaunchKernelEx(&cfg, append_slots_kernel<2>, p)
+                   : cudaLaunchKernelEx(&cfg, append_slots_kernel<1>, p);
 }
 
 cudaError_t launch_append_slots_f32(const AppendSlotsArgs& a, const float* h, const float* w_dkv,

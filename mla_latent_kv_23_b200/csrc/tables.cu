@@ -35,21 +35,27 @@ struct Request {
   bool bad;
 };
 
+// Page of a position (a shift where the page size is a power of two: a
+// division is a tenth of the small calls' time on the GPU).
+__device__ __forceinline__ int page_of(const TablesArgs& a, int p) {
+  return a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
+}
+
 __device__ __forceinline__ Request request(const TablesArgs& a, int b) {
   Request r;
   r.ctx = a.ctx_lens[b];
   r.n = a.new_lens[b];
-  const long long max_len = (long long)a.max_pages * a.page_size;
-  const long long L = (long long)r.ctx + r.n;
-  r.bad = r.ctx < 0 || r.n < 0 || L > max_len;
+  const int max_len = a.max_pages * a.page_size;
+  r.bad = r.ctx < 0 || r.n < 0 || r.ctx > max_len || r.n > max_len - r.ctx;
   if (!r.bad) {
-    r.have = r.ctx == 0 ? 0 : (r.ctx - 1) / a.page_size + 1;
+    const int L = r.ctx + r.n;
+    r.have = r.ctx == 0 ? 0 : page_of(a, r.ctx - 1) + 1;
     if (a.pages_held != nullptr) {
       const int held = a.pages_held[b];
       r.bad = held < r.have || held > a.max_pages;
       r.have = held;
     }
-    r.want = max(r.have, L == 0 ? 0 : (int)((L - 1) / a.page_size) + 1);
+    r.want = max(r.have, L == 0 ? 0 : page_of(a, L - 1) + 1);
   }
   if (r.bad) r.ctx = r.n = r.have = r.want = 0;
   return r;
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
           r = request(a, b);
           page_k = -1;
         }
-        const int q = r.ctx + (t - cu[b]), k = q / a.page_size;
+        const int q = r.ctx + (t - cu[b]), k = page_of(a, q);
         if (k != page_k) {
           page = page_at(a, b, k, r.have, (long long)used + pg[b], flags);
           page_k = k;

@@ -26,6 +26,7 @@ struct TablesArgs {
   long long* tree_mask;    // with parents
   int* err;
   int B, max_pages, n_free, max_tokens, page_size, num_pages;
+  int page_shift;  // log2 of a page size that is a power of two, else -1
 };
 cudaError_t tables_prepare();
 cudaError_t launch_build_tables(const TablesArgs& a, int sm_count, cudaStream_t s);

@@ -171,7 +171,10 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream() without building the
+        # Stream object (3 us of a call that launches in 4)
+        C = _torch()._C
+        return C._cuda_getCurrentRawStream(C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -393,29 +396,30 @@ def _int_tensor(t, name: str, shape, dtype=None):
     return t
 
 
-def _one_device(*tensors):
-    """The device that all given tensors (None aside) are on."""
-    dev = {t.device for t in tensors if t is not None}
-    if len(dev) != 1 or next(iter(dev)).type != "cuda":
-        raise ValueError("tensors must be on one CUDA device")
-    return dev.pop()
+def _one_device(*tensors) -> int:
+    """Index of the CUDA device that all given tensors (None aside) are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError("tensors must be on one CUDA device")
+    return dev
 
 
 class _On:
     """Makes a device current for a call: the library works on the current
     one.  A stream handle stays the caller's."""
+    __slots__ = ("to", "back")
 
-    def __init__(self, device):
-        self.device = device
+    def __init__(self, device: int):
+        self.to = device
 
     def __enter__(self):
-        torch = _torch()
-        self.back = torch.cuda.current_device()
-        if self.back != self.device.index:
-            torch.cuda.set_device(self.device)
+        self.back = _torch()._C._cuda_getDevice()
+        if self.back != self.to:
+            _torch().cuda.set_device(self.to)
 
     def __exit__(self, *exc):
-        if self.back != self.device.index:
+        if self.back != self.to:
             _torch().cuda.set_device(self.back)
 
 
@@ -424,6 +428,7 @@ def _keep(p, device, *tensors):
     device that the call has to be made on."""
     p.device = device
     p.tensors = tensors
+    p.ref = ctypes.byref(p)
     return p
 
 
@@ -431,15 +436,19 @@ def mla_append_latent_slots(h, W_DKV, W_KR, slots, pos, kv_cache, rope_base: flo
                             stream=None) -> None:
     """kv_cache[slots[t]] = [W_DKV h[t] || RoPE(W_KR h[t], pos[t])] for every
     token with slots[t] >= 0 (see include/mla.h)."""
+    torch = _torch()
     T, d_model = h.shape
-    d_c, d_R = W_DKV.shape[0], W_KR.shape[0]
+    d_c, k0 = W_DKV.shape
+    d_R, k1 = W_KR.shape
     rows, width = kv_cache.shape
-    if W_DKV.shape[1] != d_model or W_KR.shape[1] != d_model or width != d_c + d_R:
+    if k0 != d_model or k1 != d_model or width != d_c + d_R:
         raise ValueError("W_DKV [d_c, d_model], W_KR [d_R, d_model], kv_cache [rows, d_c + d_R] expected")
     if not h.dtype == W_DKV.dtype == W_KR.dtype == kv_cache.dtype:
         raise TypeError("h, W_DKV, W_KR and kv_cache must have one dtype")
-    _int_tensor(slots, "slots", (T,))
-    _int_tensor(pos, "pos", (T,))
+    if slots.dtype != torch.int32 or pos.dtype != torch.int32:
+        raise TypeError("slots and pos must be int32")
+    if slots.dim() != 1 or len(slots) != T or pos.dim() != 1 or len(pos) != T:
+        raise ValueError("slots and pos must have one entry per token")
     if T == 0:
         return
     with _On(_one_device(h, W_DKV, W_KR, slots, pos, kv_cache)):
@@ -486,7 +495,7 @@ def tables_params(ctx_lens, new_lens, block_table, free_pages, free_used, free_u
 def mla_build_tables(p: TablesParams, stream=None) -> None:
     """Pages, slots, positions and tree masks of a step's new tokens."""
     with _On(p.device):
-        _check(lib().mla_build_tables(ctypes.byref(p), _stream(stream)), "mla_build_tables")
+        _check(lib().mla_build_tables(p.ref, _stream(stream)), "mla_build_tables")
 
 
 def tree_params(q, kv_cache, block_table, seqlens, cu_q, tree_mask, u, lse, page_size: int, d_R: int,
@@ -532,7 +541,7 @@ def mla_decode_tree_workspace_size(p: TreeParams) -> int:
 def mla_decode_tree(p: TreeParams, workspace, stream=None) -> None:
     """Attention of drafted trees over the paged latent cache."""
     with _On(p.device):
-        _check(lib().mla_decode_tree(ctypes.byref(p), _ptr(workspace),
+        _check(lib().mla_decode_tree(p.ref, _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream)),
                "mla_decode_tree")
 
@@ -564,7 +573,7 @@ def accept_params(kv_cache, block_table, seqlens, cu_q, tree_mask, accepted, seq
 def mla_accept_tree(p: AcceptParams, stream=None) -> None:
     """The accepted branches' cache rows, moved behind their contexts."""
     with _On(p.device):
-        _check(lib().mla_accept_tree(ctypes.byref(p), _stream(stream)), "mla_accept_tree")
+        _check(lib().mla_accept_tree(p.ref, _stream(stream)), "mla_accept_tree")
 
 
 def mla_check_device_errors(stream=None) -> int:
