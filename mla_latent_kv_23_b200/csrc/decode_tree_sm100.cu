@@ -82,8 +82,8 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKv = kOffQ + kQBytes;
 constexpr uint32_t kOffP = kOffKv + kStages * kStageBytes;   // [2] second halves of P
 constexpr uint32_t kOffMax = kOffP + 2 * kPHalf;             // float [2 tile parity][64 rows]
-constexpr uint32_t kOffSum = kOffMax + 2 * 64 * 4;           // float [2 kind][2 group][64 rows]
-constexpr uint32_t kOffScratch = kOffSum + 2 * 2 * 64 * 4;    // 16 words written by the odd CTA's signals
+constexpr uint32_t kOffSum = kOffMax + 2 * 64 * 4;           // float [2 segment parity][2 kind][2 group][64 rows]
+constexpr uint32_t kOffScratch = kOffSum + 2 * 2 * 2 * 64 * 4;    // 16 words written by the odd CTA's signals
 constexpr uint32_t kOffBar = kOffScratch + 64;
 
 // Barriers of the even CTA that the odd CTA signals ("paired" below) count
@@ -103,7 +103,9 @@ enum Bar {
   Q_EMPTY,                         // last S of a segment done (paired commit)
   DEC,                             // [2] per softmax group: its 4 warps decided a tile's maximum
   GRP = DEC + 2,                   // the 8 softmax warps of this CTA
-  EPI_FREE,                        // the 8 softmax warps' output stores have read the query area
+  EPI_FREE,                        // [4] per segment (mod 4): the 8 softmax warps' output stores have
+                                   //     read the two stages that they are staged in
+  O_FREE = EPI_FREE + 4,           // even CTA, paired: the softmax warps have read a segment's O
   MMA_FINAL,                       // even CTA: all S issued so far are complete
   MMA_FINAL_PV,                    // even CTA: all P . C issued so far are complete
   BAR_COUNT
@@ -153,6 +155,51 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
           reinterpret_cast<uint64_t>(m)),
       "r"(src), "r"(x), "r"(y)
       : "memory");
+}
+
+// 16 lanes x 64 consecutive fp32 columns of TMEM, as the accumulator fragments
+// of 8 tiles of 16 x 8: v[4 i + 2 e + f] = (lane l / 4 + 8 e, column 8 i +
+// 2 (l % 4) + f) for thread l.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 lanes x 8 consecutive columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values to shared memory; lane l gives the
+// address of row l % 8 of matrix l / 8 (16 bytes) and holds of each matrix the
+// pair (row l / 4, columns 2 (l % 4) + {0, 1}).
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // Lane 0 polls (a warp of spinning lanes only adds shared-memory traffic);
@@ -230,7 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(bar(Q_FULL), 1);
     mbar_init(bar(Q_EMPTY), 1);
     mbar_init(bar(GRP), 8);
-    mbar_init(bar(EPI_FREE), 8);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(EPI_FREE + i), 8);
+    mbar_init(bar(O_FREE), 8);
     mbar_init(bar(MMA_FINAL), 1);
     mbar_init(bar(MMA_FINAL_PV), 1);
     fence_mbar_init();
@@ -266,6 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
     TreeSegment sg;
     int g = 0;
+    // A segment that ends before tile e stages its output in the stages of
+    // tiles e - 2 and e - 1, which tiles e + 2 and e + 3 take next: those wait
+    // for its stores.  epi: segments waited for; e0, e1, e2: the ends of the
+    // `open` ones after them (at most e = g - 2, g - 1 and g)
+    int epi = 0, open = 0, e0 = 0, e1 = 0, e2 = 0;
     int last_n[kStages], tail_n[kStages];  // uses of LOCAL_FULL per stage
     for (int s = 0; s < kStages; ++s) last_n[s] = -1, tail_n[s] = 0;
     bool ok = true;
@@ -304,7 +357,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (uint32_t off = 0; off < kTile; off += 16384)
               bulk_prefetch_l2(src + off, min(16384u, kTile - off));
           }
-          if (lane == 0) {
+          while (open > 0 && g >= e0 + 2) {
+            if (lane == 0 && ok)
+              ok = mbar_wait(bar(EPI_FREE + (epi & 3)), (epi >> 2) & 1, p.err, MLA_DEVFLAG_TIMEOUT);
+            ++epi;
+            --open;
+            e0 = e1;
+            e1 = e2;
+          }
+          if (lane == 0 && ok) {
             const int s = g % kStages, n = g / kStages;
             ok = mbar_wait(bar(KV_EMPTY + s), (n & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT);
             if (ok) {
@@ -337,6 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
       }
+      (open == 0 ? e0 : open == 1 ? e1 : e2) = g;
+      ++open;
     }
     // wait for this thread's tail copies in flight before the CTA may exit
     // (full tiles are consumed by the paired MMAs before the final cluster
@@ -360,11 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // CTA j], stored as row 32 qd + 16 j + i.  Rows past the block's last
       // belong to the next sequence, or read as zero behind q's end: nothing
       // of theirs is written.
-      // the query area is free once the previous segment's last S has read
-      // it and its epilogue's output stores (staged there) have left
-      if (seg_i > 0 && !(ok = warp_wait(bar(Q_EMPTY), (seg_i - 1) & 1, p.err) &&
-                              warp_wait(bar(EPI_FREE), (seg_i - 1) & 1, p.err)))
-        break;
+      // the query area is free once the previous segment's last S has read it
+      if (seg_i > 0 && !(ok = warp_wait(bar(Q_EMPTY), (seg_i - 1) & 1, p.err))) break;
       if (lane == 0) {
         const int y0 = sg.first + 64 * (int)rank;
         mbar_arrive_expect_tx(bar(Q_LOCAL), kQBytes);
@@ -517,6 +577,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; ok && j < n_t; ++j) {
             const int g = g0 + j;
             if (!(ok = warp_wait(bar(P_FULL + (g & 1)), (g >> 1) & 1, p.err))) break;
+            // the segment's first P . C overwrites O: every softmax warp of
+            // both CTAs must have read the last segment's
+            if (j == 0 && seg_i > 0 && !(ok = warp_wait(bar(O_FREE), (seg_i - 1) & 1, p.err))) break;
             issue_pv(g, j == 0);
           }
         }
@@ -543,13 +606,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int grp = sw_warp >> 2;                   // softmax group; also the O block it drains
     const int gw = sw_warp & 3;                     // warp within the group
     const int qd = warp & 3;                        // TMEM lanes [32 qd, 32 qd + 32)
-    const int jh = lane >> 4;                       // S row half: partial over CTA jh's columns
-    const int hS = 16 * qd + (lane & 15);           // row (of this CTA's 64) of this thread's S lane
+    const int rl = 16 * qd + (lane >> 2);           // this thread's S rows (of this CTA's 64): rl and rl + 8
+    const int tk = 2 * (lane & 3);                  // and their tokens: 8 i + tk + {0, 1}, i < 8
     const int hO = (32 * qd + lane) & 63;           // row of this thread's O lane
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
-    const uint32_t sw64 = static_cast<uint32_t>((hS >> 1) & 3);  // 64-byte swizzle of row hS
+    // stmatrix addresses: lane l gives row l % 8 of 8 x 8 matrix l / 8 (rows
+    // rl, rl + 8 of token group i, then of group i + 1)
+    const int pr = 16 * qd + (lane & 15), pg = lane >> 4;
+    const uint32_t sw64 = static_cast<uint32_t>((pr >> 1) & 3);  // 64-byte swizzle of row pr
     float* mx_pub = reinterpret_cast<float*>(base + kOffMax);  // [tile parity][row]
-    float* sums = reinterpret_cast<float*>(base + kOffSum);    // [kind][group][row]
+    // [kind][group][row], of two segments in turn
+    float* sums = reinterpret_cast<float*>(base + kOffSum);
+    int seg_i = 0;
     const float c_log2 = p.scale_log2;
     uint32_t grp_phase = 0;
     // A failed wait (a broken protocol) sets the device flag; the warp then
@@ -570,90 +638,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (walk.next(sg)) {
       const int n = sg.seq.n, P0 = sg.seq.L - n;  // P0: position of the first drafted token
-      // the drafted tokens that this thread's row sees (none for rows past
-      // the block's last, whose results are not written)
-      const int row_s = 64 * (int)rank + hS;
-      unsigned long long seen = 0;
-      if (row_s < sg.rows) {
-        seen = p.mask[sg.seq.row0 + (sg.g * kTreeRows + row_s) / p.n_h];
-        if (n < 64) seen &= (1ull << n) - 1;
-      }
       const int n_t = sg.t1 - sg.t0;
       const int g0 = g;
       // this group's sums over its own tiles of the segment, in the scale of
       // m_used (the maximum it last applied)
-      float m_used = -INFINITY, l = 0.f, l_exact = 0.f;
+      float m_used[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, l_exact[2] = {0.f, 0.f};
       for (int jt = (grp - g0) & 1; jt < n_t; jt += 2) {
         const int gt = g0 + jt;
-        const int t = sg.t0 + jt;
+        const int tok0 = (sg.t0 + jt) * kTreeTile;
+        // a tile that reaches into the drafted tokens: which of them this
+        // thread's rows see (none for rows past the block's last, whose
+        // results are not written), read while S of the tile runs
+        const bool tail = tok0 + kTreeTile > P0;
+        unsigned long long seen[2] = {0, 0};
+        if (tail) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 64 * (int)rank + rl + 8 * e;
+            if (r < sg.rows) seen[e] = p.mask[sg.seq.row0 + (sg.g * kTreeRows + r) / p.n_h];
+          }
+        }
         // ---- partial scores of tile gt -> registers; free the S buffer
         ok = ok && warp_wait(bar(S_FULL + grp), (gt >> 1) & 1, p.err);
         tc_fence_after();
-        // sc[16 c + k]: token 32 c + 16 jh + k of the tile, for row hS.
-        // S = partial(CTA 0 columns) + partial(CTA 1 columns): lane jh keeps
-        // tokens [16 jh, 16 jh + 16) of each 32 and hands the rest to lane ^ 16
+        // sc[4 i + 2 e + f]: row rl + 8 e, token 8 i + tk + f.  The two partials
+        // of 16 rows sit in lanes 32 qd + {0 .. 15} (CTA 0's columns, first half
+        // of the buffer's columns) and 32 qd + {16 .. 31} (CTA 1's, second
+        // half): two loads of 16 lanes put both in the same thread.
         float sc[32];
-        const uint32_t sb = tmem + lane_base + kTmemS + grp * 128;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float va[32], vb[32];
-          tmem_ld32(sb + 32 * c, va);
-          tmem_ld32(sb + 64 + 32 * c, vb);
+        {
+          const uint32_t sb = tmem + lane_base + kTmemS + grp * 128;
+          float other[32];
+          tmem_ld_16x64(sb, sc);
+          tmem_ld_16x64(sb + (16u << 16) + 64, other);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float own_lo = jh ? vb[k] : va[k], own_hi = jh ? vb[16 + k] : va[16 + k];
-            const float send = jh ? own_lo : own_hi;
-            const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
-            sc[16 * c + k] = (jh ? own_hi : own_lo) + recv;
-          }
+          for (int k = 0; k < 32; ++k) sc[k] += other[k];
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) signal_lead(S_EMPTY + grp, gw == 0, 16u, gw);
-        const int tok0 = t * kTreeTile;
         uint32_t clear_lo = 0, clear_hi = 0;  // tokens whose non-finite values must not meet P . C
-        if (tok0 + kTreeTile > P0) {
-          // the tile reaches into the drafted tokens: bit k = position tok0 + k
+        if (tail) {
+          // bit k = position tok0 + k: the context, then the drafted tokens
           const int sh = tok0 - P0;  // > -64; at most n - 1
-          const unsigned long long vis = sh >= 0 ? seen >> sh : (seen << -sh) | ((1ull << -sh) - 1);
-          uint32_t bad = 0;
+          const unsigned long long ctx = sh >= 0 ? 0 : (1ull << -sh) - 1;
+          const unsigned long long drafted = n < 64 ? (1ull << n) - 1 : ~0ull;
+          uint32_t bad[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t bits = static_cast<uint32_t>(vis >> (32 * c + 16 * jh));
+          for (int e = 0; e < 2; ++e) {
+            const unsigned long long bits = seen[e] & drafted;
+            const unsigned long long vis = (sh >= 0 ? bits >> sh : (bits << -sh) | ctx) >> tk;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              // (rows past the sequence's end are zero: their scores are finite)
-              if (!(fabsf(sc[16 * c + k]) <= 3.402823466e38f)) bad |= 1u << (16 * c + k);
-              if (!((bits >> k) & 1u)) sc[16 * c + k] = -INFINITY;
-            }
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                float& x = sc[4 * i + 2 * e + f];
+                // (rows past the sequence's end are zero: their scores are finite)
+                if (!(fabsf(x) <= 3.402823466e38f)) bad[i >> 2] |= 1u << (8 * (i & 3) + f);
+                if (!((vis >> (8 * i + f)) & 1)) x = -INFINITY;
+              }
           }
-          if (gw == 0 && __any_sync(0xffffffffu, bad != 0)) {
-            clear_lo = __reduce_or_sync(0xffffffffu, (bad & 0xffffu) << (16 * jh));
-            clear_hi = __reduce_or_sync(0xffffffffu, (bad >> 16) << (16 * jh));
+          if (gw == 0 && __any_sync(0xffffffffu, (bad[0] | bad[1]) != 0)) {
+            clear_lo = __reduce_or_sync(0xffffffffu, bad[0] << tk);
+            clear_hi = __reduce_or_sync(0xffffffffu, bad[1] << tk);
           }
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        float mx[2];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          mx0 = fmaxf(mx0, sc[k]);
-          mx1 = fmaxf(mx1, sc[k + 1]);
+        for (int e = 0; e < 2; ++e) {
+          float m0 = sc[2 * e], m1 = sc[2 * e + 1];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) {
+            m0 = fmaxf(m0, sc[4 * i + 2 * e]);
+            m1 = fmaxf(m1, sc[4 * i + 2 * e + 1]);
+          }
+          mx[e] = fmaxf(m0, m1);
         }
-        float mx = fmaxf(mx0, mx1);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
         // ---- the maximum after this tile.  The running maximum may go
         // stale: it moves only when a tile's maximum exceeds it by more than
         // 2^kRescaleThreshold (weights stay below that factor), which keeps O
         // rescales rare.  Raw scores: scale > 0 commutes with max.
-        const float t_s = mx * c_log2;
-        float m_prev = -INFINITY;
-        if (jt > 0) {  // tile gt - 1 (the other group's) is in this segment
+        if (jt > 0)  // tile gt - 1 (the other group's) is in this segment
           ok = ok && warp_wait(bar(DEC + (grp ^ 1)), ((gt - 1) >> 1) & 1, p.err);
-          m_prev = mx_pub[((gt - 1) & 1) * 64 + hS];
+        float m_new[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float t_s = mx[e] * c_log2;
+          const float m_prev = jt > 0 ? mx_pub[((gt - 1) & 1) * 64 + rl + 8 * e] : -INFINITY;
+          m_new[e] = (m_prev == -INFINITY || t_s > m_prev + kRescaleThreshold) ? fmaxf(m_prev, t_s) : m_prev;
+          if ((lane & 3) == 0) mx_pub[(gt & 1) * 64 + rl + 8 * e] = m_new[e];
         }
-        const float m_new = (m_prev == -INFINITY || t_s > m_prev + kRescaleThreshold)
-                                ? fmaxf(m_prev, t_s) : m_prev;
-        if (jh == 0) mx_pub[(gt & 1) * 64 + hS] = m_new;
         named_bar_sync(1 + grp, 128);
         // O lane hO: rescale if its row's maximum moved at this tile
         float alpha_o = 1.f;
@@ -670,28 +749,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(DEC + grp));
         // this group's sums move to the new scale
-        if (m_new != m_used) {
-          const float f = m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
-          l *= f;
-          l_exact *= f;
-          m_used = m_new;
+        float neg_m[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (m_new[e] != m_used[e]) {
+            const float f = m_used[e] == -INFINITY ? 0.f : ex2_approx(m_used[e] - m_new[e]);
+            l[e] *= f;
+            l_exact[e] *= f;
+            m_used[e] = m_new[e];
+          }
+          neg_m[e] = m_new[e] == -INFINITY ? 0.f : -m_new[e];
         }
-        const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
-        float r0 = 0.f, r1 = 0.f, e0 = 0.f, e1 = 0.f;
+        // pk[2 i + e]: the weights of row rl + 8 e, tokens 8 i + tk + {0, 1}.  u
+        // is normalised by the sum of the rounded weights it was built from;
+        // lse uses the unrounded weights
         uint32_t pk[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float a = ex2_approx(fmaf(sc[k], c_log2, neg_m));
-          const float b = ex2_approx(fmaf(sc[k + 1], c_log2, neg_m));
-          const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
-          const float2 pf = __bfloat1622float2(pr);
-          if (k & 2) { r1 += pf.x + pf.y; e1 += a + b; } else { r0 += pf.x + pf.y; e0 += a + b; }
-          pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&pr);
+        for (int e = 0; e < 2; ++e) {
+          float r0 = 0.f, r1 = 0.f, e0 = 0.f, e1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = ex2_approx(fmaf(sc[4 * i + 2 * e], c_log2, neg_m[e]));
+            const float b = ex2_approx(fmaf(sc[4 * i + 2 * e + 1], c_log2, neg_m[e]));
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+            const float2 pf = __bfloat1622float2(h2);
+            r0 += pf.x;
+            r1 += pf.y;
+            e0 += a;
+            e1 += b;
+            pk[2 * i + e] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          l[e] += r0 + r1;
+          l_exact[e] += e0 + e1;
         }
-        // u is normalised by the sum of the rounded weights it was built
-        // from; lse uses the unrounded weights
-        l += r0 + r1;
-        l_exact += e0 + e1;
 
         // P's ring slot grp was last read by PV(gt - 2); O may be rescaled
         // only after PV(gt - 1) (tiles of an earlier segment were retired by
@@ -701,30 +791,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, resc_o)) {
           ok = ok && warp_wait(bar(PV_DONE + (grp ^ 1)), ((gt - 1) >> 1) & 1, p.err);
           tc_fence_after();
-          for (int c0 = 0; c0 < 256; c0 += 32) {  // both O blocks of these lanes
-            float o[32];
-            tmem_ld32(tmem + lane_base + kTmemO + c0, o);
+          // both O blocks of these lanes, 8 columns at a time: this is rare, and
+          // its registers are the loop's
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 8) {
+            float o[8];
+            tmem_ld8(tmem + lane_base + kTmemO + c0, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha_o;
-            tmem_st32(tmem + lane_base + kTmemO + c0, o);
+            for (int i = 0; i < 8; ++i) o[i] *= alpha_o;
+            tmem_st8(tmem + lane_base + kTmemO + c0, o);
           }
           tmem_wait_st();
         }
-        // P row hS, tokens [32c + 16jh, +16): half c of the row (32 tokens =
-        // 64 B, 64-byte swizzle) lives in the stage's RoPE block (c = 0) or
-        // in ring slot grp (c = 1); 16-byte chunks 2jh and 2jh + 1
+        // P: row r, token group i (8 tokens, 16 bytes): half i / 4 of the row (32
+        // tokens = 64 B, 64-byte swizzle) lives in the stage's RoPE block or in
+        // ring slot grp
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t prow =
-              (c == 0 ? sbase + kOffKv + (gt % kStages) * kStageBytes + 4 * kKvBlk
-                      : sbase + kOffP + grp * kPHalf) + hS * 64;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t ch = static_cast<uint32_t>(2 * jh + k);
-            st_shared_v4(prow + ((ch ^ sw64) << 4), pk[8 * c + 4 * k], pk[8 * c + 4 * k + 1],
-                         pk[8 * c + 4 * k + 2], pk[8 * c + 4 * k + 3]);
-          }
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t half = i < 4 ? sbase + kOffKv + (gt % kStages) * kStageBytes + 4 * kKvBlk
+                                      : sbase + kOffP + grp * kPHalf;
+          const uint32_t ch = static_cast<uint32_t>((i & 3) + pg);
+          stmatrix_x4(half + pr * 64 + ((ch ^ sw64) << 4), pk[2 * i], pk[2 * i + 1], pk[2 * i + 2], pk[2 * i + 3]);
         }
         if (clear_lo | clear_hi) {
           // (uniform in the warp) S of this tile is done, its P . C waits for
@@ -756,21 +844,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // consecutive latent columns of O block grp)
       // the maximum after the segment's last tile (decided by either group)
       if (((g - 1) & 1) != grp) ok = ok && warp_wait(bar(DEC + (grp ^ 1)), ((g - 1) >> 1) & 1, p.err);
-      const float mS_fin = mx_pub[((g - 1) & 1) * 64 + hS];
       const float mO_fin = mx_pub[((g - 1) & 1) * 64 + hO];
       {
         // this group's sums in the scale of the final maximum
-        const float f = m_used == mS_fin ? 1.f : m_used == -INFINITY ? 0.f : ex2_approx(m_used - mS_fin);
-        const float lf = l * f, lef = l_exact * f;
-        const float l2 = lf + __shfl_xor_sync(0xffffffffu, lf, 16);
-        const float e2 = lef + __shfl_xor_sync(0xffffffffu, lef, 16);
-        if (jh == 0) {
-          sums[(0 * 2 + grp) * 64 + hS] = l2;
-          sums[(1 * 2 + grp) * 64 + hS] = e2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m_fin = mx_pub[((g - 1) & 1) * 64 + rl + 8 * e];
+          const float f = m_used[e] == m_fin ? 1.f : m_used[e] == -INFINITY ? 0.f : ex2_approx(m_used[e] - m_fin);
+          float lf = l[e] * f, lef = l_exact[e] * f;
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1) {
+            lf += __shfl_xor_sync(0xffffffffu, lf, o);
+            lef += __shfl_xor_sync(0xffffffffu, lef, o);
+          }
+          if ((lane & 3) == 0) {
+            sums[(0 * 2 + grp) * 64 + rl + 8 * e] = lf;
+            sums[(1 * 2 + grp) * 64 + rl + 8 * e] = lef;
+          }
         }
       }
-      // every warp has read the published maxima of this segment before any
-      // starts the next one
+      // every warp has read the published maxima of this segment, and the sums
+      // of the last, before any starts the next one
       ok = rendezvous(ok);
       const float l_o = sums[(0 * 2 + 0) * 64 + hO] + sums[(0 * 2 + 1) * 64 + hO];
       const float le_o = sums[(1 * 2 + 0) * 64 + hO] + sums[(1 * 2 + 1) * 64 + hO];
@@ -780,11 +874,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float inv = l_o == 0.f ? 0.f : 1.f / l_o;
       const int c = grp;                          // O block drained by this group
       const int col0 = 256 * c + 128 * (qd >> 1);  // latent column of TMEM column kTmemO + 128c
-      // The segment's last S has read Q, so the query area stages the output:
-      // 8 KB per warp, its 32 rows x 128 columns as boxes of 128-byte lines
-      // (64 bf16 or 32 fp32 columns) in the 128-byte-swizzled layout of the
-      // output tensor map (16-byte chunk k of row r at k ^ (r & 7)).
-      const uint32_t stg = sbase + kOffQ + sw_warp * 8192u;
+      // The output is staged in the stages of the segment's last tiles (those
+      // of tiles g - 2 and g - 1, whose P . C are done), 8 KB per warp: its 32
+      // rows x 128 columns as boxes of 128-byte lines (64 bf16 or 32 fp32
+      // columns) in the 128-byte-swizzled layout of the output tensor map
+      // (16-byte chunk k of row r at k ^ (r & 7)).  The next segment's queries
+      // and first two tiles load meanwhile.
+      const uint32_t stg = sbase + kOffKv + static_cast<uint32_t>((g + 2 + grp) % kStages) * kStageBytes +
+                           gw * 8192u;
       const int y_w = 64 * (int)rank + 32 * (qd & 1);  // this warp's first row of the block
       const int y_out = sg.whole ? sg.first + y_w : sg.slot * kTreeRows + y_w;
       const bool full = !sg.whole || y_w + 32 <= sg.rows;
@@ -845,13 +942,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + at)[e] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          if (full && (c0 & 32)) {  // box c0 >> 6 is complete
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&p.maps.u_out, stg + static_cast<uint32_t>(c0 >> 6) * 4096u, col0 + (c0 & 64), y_out);
-              bulk_commit();
-            }
+        }
+        if (full && !p.out_f32) {  // both boxes
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.maps.u_out, stg, col0, y_out);
+            tma_store_2d(&p.maps.u_out, stg + 4096u, col0 + 64, y_out);
+            bulk_commit();
           }
         }
       }
@@ -862,12 +960,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else if (p.lse != nullptr)
           p.lse[y_out + lane] = lse;
       }
-      // the query area may take the next segment's rows once the stores have
-      // read it
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(EPI_FREE));
+      // O has been read: the next segment's P . C may overwrite it
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        signal_lead(O_FREE, sw_warp == 0, 32u, 10);
+        // the staging area may take the next tiles once the stores have read it
+        bulk_wait_read_all();
+        mbar_arrive(bar(EPI_FREE + (seg_i & 3)));
+      }
+      __syncwarp();
+      ++seg_i;
+      sums = reinterpret_cast<float*>(base + kOffSum) + (seg_i & 1) * 256;
     }
     // the last stores complete before the CTA exits
     if (lane == 0) bulk_wait_all();

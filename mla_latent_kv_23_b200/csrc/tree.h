@@ -15,7 +15,7 @@ constexpr int kTreeRows = 128;     // (token, head) rows of one row block
 
 // Cost of one more segment inside a KV chunk (the next rows' queries, the
 // output of the last), in 64-token tiles.
-constexpr int kTreeSegTiles = 6;
+constexpr int kTreeSegTiles = 4;
 
 // Workspace of mla_decode_tree.  rec: 4 ints per chunk boundary (G + 1 of
 // them): sequence, row block and tile where the chunk starts, 0; the last one
