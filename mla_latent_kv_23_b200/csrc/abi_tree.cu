@@ -293,8 +293,8 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
   if (!aligned16(h) || !aligned16(W_DKV) || !aligned16(W_KR) || !aligned16(slots) || !aligned16(pos) ||
       !aligned16(kv_cache))
     return MLA_ERR_INVALID_ARG;
-  // the grids' limits: 65535 blocks of 256 tokens, 65535 tiles or groups of features
-  if (T > 65535 * 256 || (long long)d_c + d_R > 65535 * 32) return MLA_ERR_UNSUPPORTED;
+  // the grids' limits: 65535 tiles of 128 tokens, as many of 32 features
+  if (T > 65535 * 128 || (long long)d_c + d_R > 65535 * 32 - 64) return MLA_ERR_UNSUPPORTED;
   const DeviceInfo* d = nullptr;
   mla_status st = device_info(&d);
   if (st != MLA_OK) return st;
@@ -322,10 +322,10 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   CUtensorMap w_dkv, w_kr, x;
-  if (!rows_map(&w_dkv, W_DKV, d_c, 128) || !rows_map(&x, h, T, append_slots_tokens(T)))
+  if (!rows_map(&w_dkv, W_DKV, d_c, 32) || !rows_map(&x, h, T, append_slots_rows(T)))
     return MLA_ERR_CUDA;
   w_kr = w_dkv;
-  if (d_R > 0 && !rows_map(&w_kr, W_KR, d_R, 128)) return MLA_ERR_CUDA;
+  if (d_R > 0 && !rows_map(&w_kr, W_KR, d_R, 32)) return MLA_ERR_CUDA;
   return cuda_status(launch_append_slots(a, w_dkv, w_kr, x, s));
 }
 

@@ -2,15 +2,17 @@
 //     kv_cache[slots[t]] = [ W_DKV . h[t]  ||  RoPE(W_KR . h[t], pos[t]) ]
 // ("MLA deep compression", low-rank projection and decoupled-RoPE sections).
 //
-// bf16, on the tensor cores (sm_100a): a dense product with the 576 features
-// (128 rows of W_DKV or W_KR per tile) as M, up to 256 tokens as N and K =
-// d_model.  Few tokens are bound by reading the weights once (8.3 MB at the
-// DeepSeek-V3 shape), many by the operands' way from L2 to the SMs; both want
-// every SM at work, which five feature tiles are not.  So K is split over the
-// CTAs of a cluster, whose partial tiles (fp32) meet through distributed
-// shared memory: rank r sums the tokens r, r + cs, ... over the ranks in order
-// (the result does not depend on timing, and no scratch memory is needed),
-// rotates the RoPE features and writes whole rows of 128 features.
+// bf16, on the tensor cores (sm_100a): up to 128 tokens are the M dimension,
+// 32 j features (rows of W_DKV, then of W_KR) the N dimension, K = d_model.
+// What bounds it is the operands' way into shared memory: few tokens read the
+// weights once (8.3 MB at the DeepSeek-V3 shape), many re-read both operands
+// from L2, and an SM gets about 130 B/ns with all of its stages in flight.  So
+// K is split over the CTAs of a cluster until every SM loads, and with few
+// tokens all of a CTA's blocks are in flight at once.  The partial tiles (fp32)
+// meet through distributed shared memory: a rank sums its share of the tile over
+// the ranks in order (the result does not depend on timing, and no scratch
+// memory is needed), rotates the RoPE features and writes 16-byte-aligned runs
+// of cache rows.
 //
 // fp32: one CTA per token and 32 features on the CUDA cores.
 #include <cuda_bf16.h>
@@ -28,30 +30,53 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kWBlk = 128 * 128;  // 128 features x 64 bf16
-constexpr int kMaxTokens = 256;        // tokens per CTA
+constexpr int kTokens = 128;            // tokens per CTA, the MMA's M
+constexpr int kBox = 32;                // features per weight copy
+constexpr int kMaxBoxes = 9;            // feature boxes per CTA (N = 288 as two MMAs)
+constexpr uint32_t kBoxBytes = kBox * 128;
+constexpr int kProducers = kThreads / 32 - 1;  // warps that issue copies: all but warp 1
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStages = 8;
-constexpr uint32_t kArea = 196608;     // pipeline stages, then the fp32 partial tile
-static_assert(kArea >= kMaxTokens * 128 * 4 && kArea >= 4 * (kWBlk + kMaxTokens * 128), "area");
+constexpr int kMaxStages = 16;
+// pipeline stages, then the fp32 partial tile.  An MMA reads 128 token rows
+// from a stage's start, also where fewer were loaded (what it reads there
+// only reaches rows of D that are not used): 16 KB behind the last stage
+constexpr uint32_t kArea = 212992;
+constexpr int kPad = 4;                 // floats between rows of the partial tile
+static_assert(1 + kMaxBoxes <= 2 * kProducers && kTokens <= kThreads, "copies per producer");
+static_assert(kTokens * (kMaxBoxes * kBox + kPad) * 4 <= kArea, "the partial tile");
+static_assert(2 * (kTokens * 128 + kMaxBoxes * kBoxBytes) + kTokens * 128 <= kArea, "two stages");
 
 enum Bar { FULL = 0, EMPTY = FULL + kMaxStages, DONE = EMPTY + kMaxStages, BAR_COUNT };
 constexpr uint32_t kOffBar = kArea;
-constexpr uint32_t kOffSlot = kOffBar + BAR_COUNT * 8;
-constexpr size_t kSmem = kOffSlot + 16 + 1024;  // + alignment slack
+constexpr uint32_t kOffTmem = kOffBar + BAR_COUNT * 8;
+constexpr uint32_t kOffSlots = kOffTmem + 16;                    // int [128]
+constexpr uint32_t kOffPos = kOffSlots + kTokens * 4;            // int [128]
+constexpr uint32_t kOffTurn = kOffPos + kTokens * 4;             // double [144]
+constexpr size_t kSmem = kOffTurn + kMaxBoxes * kBox / 2 * 8 + 1024;  // + alignment slack
+static_assert(kOffTurn % 8 == 0 && kSmem <= 232448, "shared memory");
 
 struct Params {
-  CUtensorMap w_map[2];  // W_DKV, W_KR: box 64 x 128 rows
-  CUtensorMap x_map;     // h [T, K]: box 64 x n_blk rows
+  CUtensorMap w_map[2];  // W_DKV, W_KR: box 64 x 32 rows
+  CUtensorMap x_map;     // h [T, K]: box 64 x x_rows
   __nv_bfloat16* cache;
   const int* slots;
   const int* pos;
   int* err;
-  int tiles0, K, T, n_blk, stages, tmem_cols, d_c, d_R, rows;
+  int K, T, x_rows, boxes, stages, tmem_cols, d_c, d_R, rows;
   double log_base;
 };
 
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+// A whole converged warp waits (no lane is picked out and no shuffle follows:
+// those cost 150 cycles a wait).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, MLA_DEVFLAG_TIMEOUT));
+}
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -61,17 +86,19 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// (x0, x1) rotated by pos * base^(-k2 / d).  Positions reach 10^5 radians, so
-// the angle is reduced in fp64.
-__device__ __forceinline__ float2 rope_pair(float x0, float x1, int pos, double freq) {
-  const double ang = (double)pos * freq;
-  const float red = (float)(ang - 6.283185307179586 * floor(ang / 6.283185307179586));
+// (x0, x1) rotated by pos * turn full turns.  Positions reach 10^5 radians, so
+// the turns are reduced in fp64; what is left, under half a turn, is good to
+// 2^-25 of a turn in fp32.
+__device__ __forceinline__ void rotate(float& x0, float& x1, int pos, double turn) {
+  const double t = (double)pos * turn;
   float s, c;
-  sincosf(red, &s, &c);
-  return make_float2(x0 * c - x1 * s, x0 * s + x1 * c);
+  sincospif(2.f * (float)(t - rint(t)), &s, &c);
+  const float y = x0 * c - x1 * s;
+  x1 = x0 * s + x1 * c;
+  x0 = y;
 }
 
-// Grid (kCs, token blocks, feature tiles), cluster (kCs, 1, 1) along K.
+// Grid (kCs, feature tiles, token tiles), cluster (kCs, 1, 1) along K.
 template <int kCs>
 __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -79,120 +106,164 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int cs = kCs;
   const int rank = blockIdx.x;
-  const int t0 = blockIdx.y * p.n_blk;
-  const bool rope = (int)blockIdx.z >= p.tiles0;
-  const int row0 = ((int)blockIdx.z - (rope ? p.tiles0 : 0)) * 128;
+  const int t0 = blockIdx.z * kTokens, nt = min(kTokens, p.T - t0);
+  // boxes [box0, box0 + boxes) of W_DKV's nd and W_KR's nr
+  const int nd = (p.d_c + kBox - 1) / kBox, nr = (p.d_R + kBox - 1) / kBox;
+  const int box0 = blockIdx.y * p.boxes, boxes = min(p.boxes, nd + nr - box0);
   const int kb_all = p.K / 64;
-  const int kb0 = (int)((long long)kb_all * rank / cs), kb1 = (int)((long long)kb_all * (rank + 1) / cs);
-  const uint32_t xblk = p.n_blk * 128, stage = kWBlk + xblk;
+  const int kb0 = (int)((long long)kb_all * rank / kCs), kb1 = (int)((long long)kb_all * (rank + 1) / kCs);
+  const uint32_t xblk = p.x_rows * 128, stage = xblk + p.boxes * kBoxBytes;
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
+  int* slots = reinterpret_cast<int*>(base + kOffSlots);
+  int* pos = reinterpret_cast<int*>(base + kOffPos);
+  double* turns = reinterpret_cast<double*>(base + kOffTurn);
 
+  // what the epilogue needs of this thread's token, read ahead
+  const int my_slot = (int)threadIdx.x < nt ? p.slots[t0 + threadIdx.x] : -1;
+  const int my_pos = (int)threadIdx.x < nt && p.d_R > 0 ? p.pos[t0 + threadIdx.x] : 0;
+  const int copies = 1 + boxes;  // a block: the tokens, then the weight boxes
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar(FULL + s), 2);  // the two producers
+      mbar_init(bar(FULL + s), min(copies, kProducers));
       mbar_init(bar(EMPTY + s), 1);
     }
     mbar_init(bar(DONE), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(sbase + kOffSlot, p.tmem_cols);
+    tmem_alloc(sbase + kOffTmem, p.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kOffSlot);
-
-  // this warp's tokens of the epilogue, one per lane: token `lane` of them is
-  // (warp + kWarps lane) cs + rank of the block
-  const int nt = min(p.n_blk, p.T - t0);
-  const int my_t = (warp + kWarps * lane) * cs + rank;
-  const int my_slot = my_t < nt ? p.slots[t0 + my_t] : -1;
-  const int my_pos = my_t < nt && rope ? p.pos[t0 + my_t] : 0;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kOffTmem);
 
   bool ok = true;
-  if ((warp == 0 || warp == 2) && lane == 0) {
-    // producers: warp 0 the weights, warp 2 the tokens
-    const CUtensorMap* m = warp == 2 ? &p.x_map : &p.w_map[rope ? 1 : 0];
-    const uint32_t bytes = warp == 2 ? xblk : kWBlk, off = warp == 2 ? kWBlk : 0;
-    const int y = warp == 2 ? t0 : row0;
-    for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-      const int s = i % p.stages;
-      if (i >= p.stages &&
-          !(ok = mbar_wait(bar(EMPTY + s), ((i / p.stages) & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT)))
-        break;
-      mbar_arrive_expect_tx(bar(FULL + s), bytes);
-      tma_load_2d(sbase + s * stage + off, m, bar(FULL + s), kb * 64, y);
-    }
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16(128, p.n_blk, false);
-    uint32_t acc = 0;
-    for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-      const int s = i % p.stages;
-      if (!(ok = mbar_wait(bar(FULL + s), (i / p.stages) & 1, p.err, MLA_DEVFLAG_TIMEOUT))) break;
-      tc_fence_after();
-      const uint32_t st = sbase + s * stage;
-      for (int ks = 0; ks < 4; ++ks) {
-        umma_f16_ss(tmem, smem_desc(st + ks * 32, 16, 1024, kLayoutSW128),
-                    smem_desc(st + kWBlk + ks * 32, 16, 1024, kLayoutSW128), idesc, acc);
-        acc = 1;
+  if (warp != 1) {
+    // ---------------------------------------------------------- producers
+    // A block's copies and products are a few instructions, so what is done
+    // around them counts (0.49 us a block from one thread, with a division per
+    // block and descriptors built anew; 0.29 with the products from an elected
+    // thread, whose operands stay in uniform registers).  Copy k of a block is
+    // issued by warp k % 7 of the seven.
+    const int w = warp == 0 ? 0 : warp - 1;
+    if (w < copies) {
+      uint32_t phase = 0;
+      for (int kb = kb0, s = 0; kb < kb1; ++kb) {
+        if (kb - kb0 >= p.stages) {
+          if (!(ok = warp_wait(bar(EMPTY + s), phase, p.err))) break;
+        }
+        if (elect_one()) {
+          const uint32_t st = sbase + s * stage, full = bar(FULL + s);
+          const int second = w + kProducers < copies;
+          mbar_arrive_expect_tx(full, (w == 0 ? xblk : kBoxBytes) + second * kBoxBytes);
+          for (int k = w; k < copies; k += kProducers) {
+            if (k == 0) {
+              tma_load_2d(st, &p.x_map, full, kb * 64, t0);
+            } else {
+              const int box = box0 + k - 1;
+              tma_load_2d(st + xblk + (k - 1) * kBoxBytes, &p.w_map[box < nd ? 0 : 1], full, kb * 64,
+                          (box < nd ? box : box - nd) * kBox);
+            }
+          }
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          if (kb - kb0 >= p.stages) phase ^= 1;
+        }
       }
-      umma_commit(bar(EMPTY + s));
     }
-    umma_commit(bar(DONE));
+    // meanwhile: the turns of the tile's RoPE pairs, by pair within the tile
+    for (int i = w * 32 + lane; i < boxes * kBox / 2; i += kProducers * 32) {
+      const int f = (box0 - nd) * kBox + 2 * i;  // of the RoPE key
+      if (f >= 0) turns[i] = exp(-(double)f / (double)p.d_R * p.log_base) * 0.15915494309189535;
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const int n = p.boxes * kBox, parts = n > 256 ? 2 : 1;  // (N is at most 256)
+    const uint32_t idesc = idesc_bf16(kTokens, n / parts, false);
+    const uint64_t x0 = smem_desc(sbase, 16, 1024, kLayoutSW128);
+    const uint64_t w0 = smem_desc(sbase + xblk, 16, 1024, kLayoutSW128);
+    const uint32_t step = stage >> 4, half = (n / 2 * 128) >> 4;  // in a descriptor's 16-byte units
+    uint32_t phase = 0, at = 0;
+    for (int kb = kb0, s = 0; kb < kb1; ++kb) {
+      if (!(ok = warp_wait(bar(FULL + s), phase, p.err))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t acc = ks > 0 || kb > kb0;
+          umma_f16_ss(tmem, x0 + at + 2 * ks, w0 + at + 2 * ks, idesc, acc);
+          if (parts == 2) umma_f16_ss(tmem + n / 2, x0 + at + 2 * ks, w0 + at + half + 2 * ks, idesc, acc);
+        }
+        umma_commit(bar(EMPTY + s));
+        if (kb == kb1 - 1) umma_commit(bar(DONE));
+      }
+      __syncwarp();
+      at += step;
+      if (++s == p.stages) s = 0, phase ^= 1, at = 0;
+    }
+  }
+  if ((int)threadIdx.x < nt) {
+    slots[threadIdx.x] = my_slot;
+    pos[threadIdx.x] = my_pos;
   }
   __syncwarp();
-  if (threadIdx.x == 0) ok = mbar_wait(bar(DONE), 0, p.err, MLA_DEVFLAG_TIMEOUT) && ok;
+  if (threadIdx.x == 32 && ok) ok = mbar_wait(bar(DONE), 0, p.err, MLA_DEVFLAG_TIMEOUT);
   ok = __syncthreads_and(ok);
   tc_fence_after();
-  // the partial tile as [token][128 features] in the pipeline's area (every
-  // load has been consumed): TMEM lane = feature, column = token
-  float* part = reinterpret_cast<float*>(base);
-  const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  for (int c0 = (warp >> 2) * 32; c0 < p.n_blk; c0 += 64) {
-    float v[32];
-    tmem_ld32(tmem + lane_base + c0, v);
-    tmem_wait_ld();
+  // the partial tile as [token][feature] in the pipeline's area (every load
+  // has been consumed): TMEM lane = token, column = feature; the four spare
+  // floats per row keep eight lanes' 16-byte stores on different banks
+  const int ld = p.boxes * kBox + kPad;
+  {
+    const int t = (warp & 3) * 32 + lane;
+    float* row = reinterpret_cast<float*>(base) + t * ld;
+    const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    if ((warp & 3) * 32 < nt)
+      for (int c0 = (warp >> 2) * 32; c0 < boxes * kBox; c0 += 64) {
+        float v[32];
+        tmem_ld32(at + c0, v);
+        tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (c0 + k < p.n_blk) part[(c0 + k) * 128 + (warp & 3) * 32 + lane] = v[k];
+        for (int k = 0; k < 32; k += 4)
+          *reinterpret_cast<float4*>(row + c0 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      }
   }
   tc_fence_before();
   cluster_sync();
-  // one warp per token, four features per lane
-  const int f = row0 + 4 * lane;
+  // this rank's share of the tile: runs of four features, token-major
+  const int quads = boxes * kBox / 4, all = nt * quads;
+  const int share = (all + kCs - 1) / kCs, end = min(all, share * (rank + 1));
   const int width = p.d_c + p.d_R;
-  const bool live = ok && f < (rope ? p.d_R : p.d_c);
-  const double freq0 = rope ? exp(-(double)f / (double)p.d_R * p.log_base) : 0.0;
-  const double freq1 = rope ? exp(-(double)(f + 2) / (double)p.d_R * p.log_base) : 0.0;
-  for (int k = 0; k < (kMaxTokens + kWarps * cs - 1) / (kWarps * cs); ++k) {
-    const int t = (warp + kWarps * k) * cs + rank;
-    if (t >= nt) break;
-    const int slot = __shfl_sync(0xffffffffu, my_slot, k), pos = __shfl_sync(0xffffffffu, my_pos, k);
-    if (slot < 0) continue;
-    if (slot >= p.rows) {
-      if (lane == 0) atomicOr(p.err, MLA_DEVFLAG_BAD_PAGE);
-      continue;
-    }
-    const uint32_t at = sbase + (t * 128 + 4 * lane) * 4;
-    float4 y[cs];
+  for (int i = share * rank + (int)threadIdx.x; i < end; i += kThreads) {
+    const int t = i / quads, q = i - t * quads;
+    const uint32_t at = sbase + (t * ld + 4 * q) * 4;
+    float4 y[kCs];
 #pragma unroll
-    for (int r = 0; r < cs; ++r) y[r] = ld_cluster_v4(mapa(at, r));
+    for (int r = 0; r < kCs; ++r) y[r] = ld_cluster_v4(mapa(at, r));
     float4 x = y[0];
 #pragma unroll
-    for (int r = 1; r < cs; ++r) {
+    for (int r = 1; r < kCs; ++r) {
       x.x += y[r].x;
       x.y += y[r].y;
       x.z += y[r].z;
       x.w += y[r].w;
     }
-    if (!live) continue;
+    const int slot = slots[t];
+    const bool rope = box0 + q / 8 >= nd;
+    const int f = 4 * q + (rope ? (box0 - nd) * kBox : box0 * kBox);
+    if (!ok || slot < 0 || f >= (rope ? p.d_R : p.d_c)) continue;
+    if (slot >= p.rows) {
+      atomicOr(p.err, MLA_DEVFLAG_BAD_PAGE);
+      continue;
+    }
     if (rope) {
-      const float2 a = rope_pair(x.x, x.y, pos, freq0), b = rope_pair(x.z, x.w, pos, freq1);
-      x = make_float4(a.x, a.y, b.x, b.y);
+      rotate(x.x, x.y, pos[t], turns[2 * q]);
+      rotate(x.z, x.w, pos[t], turns[2 * q + 1]);
     }
     const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
     uint2 w;
@@ -262,12 +333,8 @@ int append_slots_prepare() {
   return 1;
 }
 
-// Tokens per CTA: T in as few blocks of up to 256 as there have to be, all
-// alike, in steps of 16 (the MMA's N).
-int append_slots_tokens(int T) {
-  const int blocks = (T + kMaxTokens - 1) / kMaxTokens;
-  return ((T + blocks - 1) / blocks + 15) / 16 * 16;
-}
+// Token rows of one copy: T up to a whole 8-row group, 128 at most.
+int append_slots_rows(int T) { return std::min(kTokens, (T + 7) / 8 * 8); }
 
 cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_dkv,
                                 const CUtensorMap& w_kr, const CUtensorMap& x, cudaStream_t s) {
@@ -279,26 +346,38 @@ cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_d
   p.slots = a.slots;
   p.pos = a.pos;
   p.err = a.err;
-  p.tiles0 = (a.d_c + 127) / 128;
   p.K = a.d_model;
   p.T = a.T;
-  p.n_blk = append_slots_tokens(a.T);
-  p.stages = std::min<int>(kMaxStages, kArea / (kWBlk + p.n_blk * 128));
-  p.tmem_cols = 32;
-  while (p.tmem_cols < p.n_blk) p.tmem_cols *= 2;
+  p.x_rows = append_slots_rows(a.T);
   p.d_c = a.d_c;
   p.d_R = a.d_R;
   p.rows = a.rows;
   p.log_base = log(a.rope_base);
-  const int tiles = p.tiles0 + (a.d_R > 0 ? (a.d_R + 127) / 128 : 0);
-  const int blocks = (a.T + p.n_blk - 1) / p.n_blk;
-  // K over as many CTAs as fill the SMs once (powers of two: a cluster sits in
-  // one GPC, and others would leave SMs of it idle), each with 4 blocks of 64
-  // columns or more
+  const int total = (a.d_c + kBox - 1) / kBox + (a.d_R + kBox - 1) / kBox;
+  const int token_tiles = (a.T + kTokens - 1) / kTokens, kb = a.d_model / 64;
+  // Boxes per CTA and CTAs along K.
   int cs = 1;
-  while (2 * cs <= kMaxCluster && 2 * cs * tiles * blocks <= a.sm_count && 2 * cs * 256 <= a.d_model) cs *= 2;
+  p.boxes = 1;
+  double best = 0;
+  for (int j = 1; j <= std::min(kMaxBoxes, total); ++j)
+    for (int c = 1; c <= kMaxCluster && c <= kb; c *= 2) {
+      const int ctas = (total + j - 1) / j * token_tiles * c;
+      const int waves = (ctas + a.sm_count - 1) / a.sm_count;
+      const double load = (double)((kb + c - 1) / c) * (p.x_rows * 128 + j * kBoxBytes) / 130.0;
+      const double reduce = (double)std::min(a.T, kTokens) * j * kBox * 4 / 100.0;
+      const double t = waves * (load + reduce + 3000);
+      if (best == 0 || t < best) {
+        best = t;
+        p.boxes = j;
+        cs = c;
+      }
+    }
+  const uint32_t stage = p.x_rows * 128 + p.boxes * kBoxBytes;
+  p.stages = std::min<int>(kMaxStages, (kArea - kTokens * 128) / stage);
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.boxes * kBox) p.tmem_cols *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, blocks, tiles);
+  cfg.gridDim = dim3(cs, (total + p.boxes - 1) / p.boxes, token_tiles);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;

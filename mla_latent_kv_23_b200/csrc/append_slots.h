@@ -14,8 +14,8 @@ struct AppendSlotsArgs {
   double rope_base;
 };
 int append_slots_prepare();
-int append_slots_tokens(int T);  // token rows of the x map's box
-// w maps: box 64 x 128 rows; x map: box 64 x append_slots_tokens(T); bf16, 128-byte swizzle
+int append_slots_rows(int T);  // token rows of the x map's box
+// w maps: box 64 x 32 rows; x map: box 64 x append_slots_rows(T); bf16, 128-byte swizzle
 cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_dkv,
                                 const CUtensorMap& w_kr, const CUtensorMap& x, cudaStream_t s);
 cudaError_t launch_append_slots_f32(const AppendSlotsArgs& a, const float* h, const float* w_dkv,

@@ -202,32 +202,28 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
-// Lane 0 polls (a warp of spinning lanes only adds shared-memory traffic);
-// the shuffle hands the outcome, and the ordering, to the rest of the warp.
-template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait<kCluster>(bar, parity, err, MLA_DEVFLAG_TIMEOUT);
-  return __shfl_sync(0xffffffffu, ok, 0);
+// One thread of a converged warp, always the same.  Instructions that take
+// uniform registers (MMA, TMA, commits) come from an elected thread: behind
+// `lane == 0` the compiler cannot keep their operands uniform, and a warp that
+// waits as a whole needs no shuffle after it.  Both together, against lane 0
+// waiting and issuing: 16 trees of 64 tokens over 4096 1556 -> 1440 us, 37 over
+// 256 355 -> 313, one token over 70 23.4 -> 20.5.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 
-// Both phases complete; the two tests of each poll are independent, so their
-// shared-memory latencies overlap.
+// Waits of a whole converged warp; a failed one (its time ran out) fails for
+// every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, MLA_DEVFLAG_TIMEOUT));
+}
 __device__ __forceinline__ bool warp_wait2(uint32_t bar0, uint32_t par0, uint32_t bar1,
                                            uint32_t par1, int* err) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
-    const uint64_t t0 = cycles();
-    uint32_t n = 0;
-    while (!(mbar_test_nb(bar0, par0) & mbar_test_nb(bar1, par1))) {
-      if ((++n & 31u) == 0 && cycles() - t0 > kWaitLimitCycles) {
-        atomicOr(err, MLA_DEVFLAG_TIMEOUT);
-        ok = false;
-        break;
-      }
-    }
-  }
-  return __shfl_sync(0xffffffffu, ok, 0);
+  const bool a = mbar_wait(bar0, par0, err, MLA_DEVFLAG_TIMEOUT);
+  const bool b = mbar_wait(bar1, par1, err, MLA_DEVFLAG_TIMEOUT);
+  return __all_sync(0xffffffffu, a && b);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -319,8 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // for its stores.  epi: segments waited for; e0, e1, e2: the ends of the
     // `open` ones after them (at most e = g - 2, g - 1 and g)
     int epi = 0, open = 0, e0 = 0, e1 = 0, e2 = 0;
-    int last_n[kStages], tail_n[kStages];  // uses of LOCAL_FULL per stage
-    for (int s = 0; s < kStages; ++s) last_n[s] = -1, tail_n[s] = 0;
+    uint32_t tail_used = 0, tail_phase = 0;  // stages that held a tail tile; parity of its LOCAL_FULL's next phase
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int* bt = p.block_table + (size_t)sg.b * p.max_pages;
@@ -349,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // first stages; fetching more then only delays those, so the first
           // kStages tiles of the chunk prefetch nothing.
           const int page_ahead = __shfl_sync(0xffffffffu, my_page, (i + kPrefetchAhead) & 31);
-          if (leader && lane == 0 && g >= kStages && i + kPrefetchAhead < n_here) {
+          if (leader && g >= kStages && i + kPrefetchAhead < n_here && elect_one()) {
             const int tok_a = (t0 + i + kPrefetchAhead) * kTreeTile;
             const uint8_t* src = reinterpret_cast<const uint8_t*>(
                 p.kv + ((size_t)page_ahead * p.page_size + tok_a % p.page_size) * (kDc + 64));
@@ -358,64 +353,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               bulk_prefetch_l2(src + off, min(16384u, kTile - off));
           }
           while (open > 0 && g >= e0 + 2) {
-            if (lane == 0 && ok)
-              ok = mbar_wait(bar(EPI_FREE + (epi & 3)), (epi >> 2) & 1, p.err, MLA_DEVFLAG_TIMEOUT);
+            ok = ok && warp_wait(bar(EPI_FREE + (epi & 3)), (epi >> 2) & 1, p.err);
             ++epi;
             --open;
             e0 = e1;
             e1 = e2;
           }
-          if (lane == 0 && ok) {
-            const int s = g % kStages, n = g / kStages;
-            ok = mbar_wait(bar(KV_EMPTY + s), (n & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT);
-            if (ok) {
-              const int tok = (t0 + i) * kTreeTile;
-              const int y = page * p.page_size + tok % p.page_size;
-              const uint32_t st = sbase + kOffKv + s * kStageBytes;
-              if (L - tok < kTreeTile) {
-                // tail tile: this CTA's relay zeroes the rows past the end
-                // once they land, then signals the even CTA
-                mbar_arrive_expect_tx(bar(LOCAL_FULL + s), kStageBytes);
-                tma_load_4d_hint(st, &p.maps.kv_lat4, bar(LOCAL_FULL + s), 128 * (int)rank, y, 0, 0,
-                                 pol_stream);
-                tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(LOCAL_FULL + s),
-                                 kDc + 32 * (int)rank, y, pol_stream);
-                last_n[s] = tail_n[s]++;
-              } else if (leader) {
-                // full tile: both CTAs' bytes complete on the even CTA's barrier
-                mbar_arrive_expect_tx(bar(KV_FULL + s), 2 * kStageBytes);
-                tma_load_4d_hint(st, &p.maps.kv_lat4, bar(KV_FULL + s), 0, y, 0, 0, pol_stream);
-                tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(KV_FULL + s), kDc, y,
-                                 pol_stream);
-              } else {
-                const uint32_t full = mapa(bar(KV_FULL + s), 0);
-                tma_load_4d_to_pair_hint(st, &p.maps.kv_lat4, full, 128, y, 0, 0, pol_stream);
-                tma_load_2d_to_pair_hint(st + 4 * kKvBlk, &p.maps.kv_rope, full, kDc + 32, y, pol_stream);
-              }
+          const int s = g % kStages;
+          if (!(ok = ok && warp_wait(bar(KV_EMPTY + s), ((g / kStages) & 1) ^ 1, p.err))) break;
+          const int tok = (t0 + i) * kTreeTile;
+          const int y = page * p.page_size + tok % p.page_size;
+          const uint32_t st = sbase + kOffKv + s * kStageBytes;
+          const bool tail = L - tok < kTreeTile;
+          if (elect_one()) {
+            if (tail) {
+              // this CTA's relay zeroes the rows past the end once they land,
+              // then signals the even CTA
+              mbar_arrive_expect_tx(bar(LOCAL_FULL + s), kStageBytes);
+              tma_load_4d_hint(st, &p.maps.kv_lat4, bar(LOCAL_FULL + s), 128 * (int)rank, y, 0, 0,
+                               pol_stream);
+              tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(LOCAL_FULL + s),
+                               kDc + 32 * (int)rank, y, pol_stream);
+            } else if (leader) {
+              // full tile: both CTAs' bytes complete on the even CTA's barrier
+              mbar_arrive_expect_tx(bar(KV_FULL + s), 2 * kStageBytes);
+              tma_load_4d_hint(st, &p.maps.kv_lat4, bar(KV_FULL + s), 0, y, 0, 0, pol_stream);
+              tma_load_2d_hint(st + 4 * kKvBlk, &p.maps.kv_rope, bar(KV_FULL + s), kDc, y, pol_stream);
+            } else {
+              const uint32_t full = mapa(bar(KV_FULL + s), 0);
+              tma_load_4d_to_pair_hint(st, &p.maps.kv_lat4, full, 128, y, 0, 0, pol_stream);
+              tma_load_2d_to_pair_hint(st + 4 * kKvBlk, &p.maps.kv_rope, full, kDc + 32, y, pol_stream);
             }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
+          __syncwarp();
+          if (tail) {
+            tail_used |= 1u << s;
+            tail_phase ^= 1u << s;
+          }
         }
       }
       (open == 0 ? e0 : open == 1 ? e1 : e2) = g;
       ++open;
     }
-    // wait for this thread's tail copies in flight before the CTA may exit
-    // (full tiles are consumed by the paired MMAs before the final cluster
-    // barrier)
-    if (lane == 0)
-      for (int s = 0; s < kStages; ++s)
-        if (last_n[s] >= 0) mbar_wait(bar(LOCAL_FULL + s), last_n[s] & 1, p.err, MLA_DEVFLAG_TIMEOUT);
-    __syncwarp();
+    // this CTA's tail copies land before it may exit (full tiles are consumed
+    // by the paired MMAs before the final cluster barrier)
+    for (int s = 0; s < kStages; ++s)
+      if ((tail_used >> s) & 1) warp_wait(bar(LOCAL_FULL + s), ((tail_phase >> s) & 1) ^ 1, p.err);
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     TreeWalk walk;
     walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
     TreeSegment sg;
     int g = 0, seg_i = 0;
-    int tail_n[kStages];  // uses of LOCAL_FULL per stage, in tile order
-    for (int s = 0; s < kStages; ++s) tail_n[s] = 0;
+    uint32_t tail_phase = 0;  // parity of each stage's next LOCAL_FULL phase
     bool ok = true;
     bool q_in_flight = false;
     while (ok && walk.next(sg)) {
@@ -425,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // of theirs is written.
       // the query area is free once the previous segment's last S has read it
       if (seg_i > 0 && !(ok = warp_wait(bar(Q_EMPTY), (seg_i - 1) & 1, p.err))) break;
-      if (lane == 0) {
+      if (elect_one()) {
         const int y0 = sg.first + 64 * (int)rank;
         mbar_arrive_expect_tx(bar(Q_LOCAL), kQBytes);
         if (p.maps.has_q4) {
@@ -470,7 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int s = g % kStages;
         const int rows_valid = L - t * kTreeTile;
         if (rows_valid >= kTreeTile) continue;  // full tile: no relay
-        if (!(ok = warp_wait(bar(LOCAL_FULL + s), (tail_n[s]++) & 1, p.err))) break;
+        if (!(ok = warp_wait(bar(LOCAL_FULL + s), (tail_phase >> s) & 1, p.err))) break;
+        tail_phase ^= 1u << s;
         // rows past the sequence end may hold anything; make them zero so
         // that 0-probability x garbage cannot turn into NaN in P . C
         uint8_t* tile = base + kOffKv + s * kStageBytes;
@@ -491,8 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++seg_i;
     }
     // a query copy still in flight must land before the CTA may exit
-    if (q_in_flight && lane == 0) mbar_wait(bar(Q_LOCAL), seg_i & 1, p.err, MLA_DEVFLAG_TIMEOUT);
-    __syncwarp();
+    if (q_in_flight) warp_wait(bar(Q_LOCAL), seg_i & 1, p.err);
   } else if (warp == kWarpMma || warp == kWarpAlloc) {
     // ------------------------------------------------------------ MMA issuers
     // Warp 1 issues every S, warp 2 (done allocating) every P . C.  The two
@@ -508,26 +498,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       TreeSegment sg;
       int g0 = 0, seg_i = 0;
       bool ok = true;
+      // Descriptors are the first tile's plus a distance in 16-byte units: the
+      // one thread that issues has 18 products a tile to keep the pipe fed
+      const uint64_t q_lat = smem_desc(sbase + kOffQ, 16, 1024, kLayoutSW128);
+      const uint64_t q_rope = smem_desc(sbase + kOffQ + 4 * kQBlk, 16, 512, kLayoutSW64);
+      const uint64_t k_lat = smem_desc(sbase + kOffKv, 16, 1024, kLayoutSW128);
+      const uint64_t k_rope = smem_desc(sbase + kOffKv + 4 * kKvBlk, 16, 512, kLayoutSW64);
+      const uint64_t v_lat = smem_desc(sbase + kOffKv, kKvBlk, 1024, kLayoutSW128);
+      const uint64_t p_ring = smem_desc(sbase + kOffP, 16, 512, kLayoutSW64);
       // S for global tile g: 16 steps over the latent columns, 2 over RoPE
       auto issue_s = [&](int g, bool last) {
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t st = sbase + kOffKv + (g % kStages) * kStageBytes;
+        if (elect_one()) {
+          const uint32_t st = (g % kStages) * (kStageBytes >> 4);
           const uint32_t dS = tmem + kTmemS + (g & 1) * 128;
-          uint32_t acc = 0;
+#pragma unroll
           for (int kc = 0; kc < 4; ++kc)
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t a =
-                  smem_desc(sbase + kOffQ + kc * kQBlk + ks * 32, 16, 1024, kLayoutSW128);
-              const uint64_t b = smem_desc(st + kc * kKvBlk + ks * 32, 16, 1024, kLayoutSW128);
-              umma_f16_ss_pair(dS, a, b, kIdS, acc);
-              acc = 1;
-            }
-          for (int ks = 0; ks < 2; ++ks) {
-            const uint64_t a = smem_desc(sbase + kOffQ + 4 * kQBlk + ks * 32, 16, 512, kLayoutSW64);
-            const uint64_t b = smem_desc(st + 4 * kKvBlk + ks * 32, 16, 512, kLayoutSW64);
-            umma_f16_ss_pair(dS, a, b, kIdS, 1u);
-          }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ss_pair(dS, q_lat + kc * (kQBlk >> 4) + ks * 2,
+                               k_lat + st + kc * (kKvBlk >> 4) + ks * 2, kIdS, kc + ks > 0 ? 1u : 0u);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            umma_f16_ss_pair(dS, q_rope + ks * 2, k_rope + st + ks * 2, kIdS, 1u);
           umma_commit_pair(bar(S_FULL + (g & 1)), kBothCtas);
           if (last) umma_commit_pair(bar(Q_EMPTY), kBothCtas);
         }
@@ -536,19 +529,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // O (+)= P . C for global tile g; `first` = first tile of its segment
       auto issue_pv = [&](int g, bool first) {
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t st = sbase + kOffKv + (g % kStages) * kStageBytes;
+        if (elect_one()) {
+          const uint32_t st = (g % kStages) * (kStageBytes >> 4);
           // P tokens 0-31 sit in the stage's RoPE block (S is done with it),
           // tokens 32-63 in the second-half ring
-          const uint32_t pa0 = st + 4 * kKvBlk, pa1 = sbase + kOffP + (g & 1) * kPHalf;
+          const uint64_t pa[2] = {k_rope + st, p_ring + (g & 1) * (kPHalf >> 4)};
+#pragma unroll
           for (int blk = 0; blk < 2; ++blk)
-            for (int kk = 0; kk < 4; ++kk) {  // 16 tokens per MMA
-              const uint64_t a = smem_desc((kk < 2 ? pa0 : pa1) + (kk & 1) * 32, 16, 512, kLayoutSW64);
-              const uint64_t b =
-                  smem_desc(st + 2 * blk * kKvBlk + kk * 2048, kKvBlk, 1024, kLayoutSW128);
-              umma_f16_ss_pair(tmem + kTmemO + blk * 128, a, b, kIdPV,
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 tokens per MMA
+              umma_f16_ss_pair(tmem + kTmemO + blk * 128, pa[kk >> 1] + (kk & 1) * 2,
+                               v_lat + st + 2 * blk * (kKvBlk >> 4) + kk * (2048 >> 4), kIdPV,
                                (first && kk == 0) ? 0u : 1u);
-            }
           umma_commit_pair(bar(KV_EMPTY + g % kStages), kBothCtas);
           umma_commit_pair(bar(PV_DONE + (g & 1)), kBothCtas);
         }
@@ -588,11 +580,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // every MMA issued by this thread has completed before TMEM is freed
       const int fin = s_issuer ? MMA_FINAL : MMA_FINAL_PV;
-      if (lane == 0) {
-        umma_commit_pair(bar(fin), 1);
-        mbar_wait(bar(fin), 0, p.err, MLA_DEVFLAG_TIMEOUT);
-      }
-      __syncwarp();
+      if (elect_one()) umma_commit_pair(bar(fin), 1);
+      warp_wait(bar(fin), 0, p.err);
     }
   } else if (warp >= kWarpSoftmax0) {
     // ------------------------------------------------------------ softmax
