@@ -63,7 +63,7 @@ mla_status device_info(const DeviceInfo** out) {
     d.small_tc = (d.cc_major == 10) && decode_small_sm100_prepare() != 0;
     d.up_proj_tc = (d.cc_major == 10) && up_proj_sm100_prepare() != 0;
     d.wgemm_tc = (d.cc_major == 10) && wgemm_sm100_prepare() != 0;
-    d.append_tc = (d.cc_major == 10) && append_slots_prepare() != 0;
+    d.append_tc = (d.cc_major == 10) && append_slots_prepare(d.append_clusters);
     if ((e = tables_prepare()) != cudaSuccess) return cuda_status(e);
     if (g_encode == nullptr) {
       cudaDriverEntryPointQueryResult q;

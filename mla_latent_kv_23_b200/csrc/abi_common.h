@@ -7,6 +7,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "append_slots.h"
 #include "mla.h"
 
 namespace mla {
@@ -21,6 +22,7 @@ struct DeviceInfo {
   bool up_proj_tc = false;
   bool wgemm_tc = false;  // the weight-streaming projection kernel is usable
   bool append_tc = false;  // the slot-map append kernel is usable
+  int append_clusters[kClusterSizes] = {};  // its co-resident clusters by size
   int* flags = nullptr;  // device address of the sticky device flags
 };
 

@@ -54,8 +54,15 @@ bool tree_v3(const mla_tree_params* p, const DeviceInfo* d) {
          p->dtype == MLA_DTYPE_BF16 && p->d_c == 512 && p->d_R == 64;
 }
 
+// One chunk per resident cluster, but no more than the batch can have tiles by
+// what the host knows (row blocks times the block table's width): starting and
+// retiring 148 CTAs of 226 KB takes longer than the work of a small call.
 int tree_chunks(const mla_tree_params* p, const DeviceInfo* d) {
-  return p->num_splits > 0 ? p->num_splits : d->tree_clusters;
+  if (p->num_splits > 0) return p->num_splits;
+  const long long blocks = p->B + (long long)p->T * p->n_h / kTreeRows;
+  const long long tiles = (long long)p->max_pages_per_seq * p->page_size / kTreeTile;
+  const long long most = blocks * tiles;
+  return most < d->tree_clusters ? (int)(most < 1 ? 1 : most) : d->tree_clusters;
 }
 
 mla_status encode_tree(TreeMaps* m, const mla_tree_params* p, const TreeArgs& a) {
@@ -309,7 +316,7 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
   a.d_c = d_c;
   a.d_R = d_R;
   a.rows = cache_rows;
-  a.sm_count = d->sm_count;
+  a.max_clusters = d->append_clusters;
   a.rope_base = rope_base;
   if (dtype == MLA_DTYPE_FP32)
     return cuda_status(launch_append_slots_f32(a, static_cast<const float*>(h),

@@ -35,7 +35,6 @@ constexpr int kBox = 32;                // features per weight copy
 constexpr int kMaxBoxes = 9;            // feature boxes per CTA (N = 288 as two MMAs)
 constexpr uint32_t kBoxBytes = kBox * 128;
 constexpr int kProducers = kThreads / 32 - 1;  // warps that issue copies: all but warp 1
-constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 16;
 // pipeline stages, then the fp32 partial tile.  An MMA reads 128 token rows
 // from a stage's start, also where fewer were loaded (what it reads there
@@ -72,8 +71,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
-// A whole converged warp waits (no lane is picked out and no shuffle follows:
-// those cost 150 cycles a wait).
+// A whole converged warp waits; a failed wait fails for every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, MLA_DEVFLAG_TIMEOUT));
 }
@@ -144,10 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
   if (warp != 1) {
     // ---------------------------------------------------------- producers
     // A block's copies and products are a few instructions, so what is done
-    // around them counts (0.49 us a block from one thread, with a division per
-    // block and descriptors built anew; 0.29 with the products from an elected
-    // thread, whose operands stay in uniform registers).  Copy k of a block is
-    // issued by warp k % 7 of the seven.
+    // around them counts: 0.49 us a block with both behind `lane == 0`, a
+    // division per block and descriptors built anew; 0.22 with an elected
+    // thread for the products (its operands stay in uniform registers) and the
+    // copies of a block spread over seven warps, copy k on warp k % 7.
     const int w = warp == 0 ? 0 : warp - 1;
     if (w < copies) {
       uint32_t phase = 0;
@@ -189,10 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
     const uint64_t w0 = smem_desc(sbase + xblk, 16, 1024, kLayoutSW128);
     const uint32_t step = stage >> 4, half = (n / 2 * 128) >> 4;  // in a descriptor's 16-byte units
     uint32_t phase = 0, at = 0;
-    for (int kb = kb0, s = 0; kb < kb1; ++kb) {
-      if (!(ok = warp_wait(bar(FULL + s), phase, p.err))) break;
-      tc_fence_after();
-      if (elect_one()) {
+    if (elect_one()) {
+      for (int kb = kb0, s = 0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(bar(FULL + s), phase, p.err, MLA_DEVFLAG_TIMEOUT))) break;
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint32_t acc = ks > 0 || kb > kb0;
@@ -200,11 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
           if (parts == 2) umma_f16_ss(tmem + n / 2, x0 + at + 2 * ks, w0 + at + half + 2 * ks, idesc, acc);
         }
         umma_commit(bar(EMPTY + s));
-        if (kb == kb1 - 1) umma_commit(bar(DONE));
+        at += step;
+        if (++s == p.stages) s = 0, phase ^= 1, at = 0;
       }
-      __syncwarp();
-      at += step;
-      if (++s == p.stages) s = 0, phase ^= 1, at = 0;
+      umma_commit(bar(DONE));
+      ok = mbar_wait(bar(DONE), 0, p.err, MLA_DEVFLAG_TIMEOUT) && ok;
     }
   }
   if ((int)threadIdx.x < nt) {
@@ -212,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
     pos[threadIdx.x] = my_pos;
   }
   __syncwarp();
-  if (threadIdx.x == 32 && ok) ok = mbar_wait(bar(DONE), 0, p.err, MLA_DEVFLAG_TIMEOUT);
   ok = __syncthreads_and(ok);
   tc_fence_after();
   // the partial tile as [token][feature] in the pipeline's area (every load
@@ -321,16 +318,29 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-int append_slots_prepare() {
-  auto prepare = [](auto kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) == cudaSuccess;
+bool append_slots_prepare(int (&max_clusters)[kClusterSizes]) {
+  auto prepare = [&](auto kernel, int e) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+      return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 << e, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << e;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&max_clusters[e], kernel, &cfg) == cudaSuccess && max_clusters[e] > 0;
   };
-  if (!prepare(append_slots_kernel<1>) || !prepare(append_slots_kernel<2>) ||
-      !prepare(append_slots_kernel<4>) || !prepare(append_slots_kernel<8>)) {
+  if (!prepare(append_slots_kernel<1>, 0) || !prepare(append_slots_kernel<2>, 1) ||
+      !prepare(append_slots_kernel<4>, 2) || !prepare(append_slots_kernel<8>, 3)) {
     cudaGetLastError();
-    return 0;
+    return false;
   }
-  return 1;
+  return true;
 }
 
 // Token rows of one copy: T up to a whole 8-row group, 128 at most.
@@ -355,21 +365,26 @@ cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_d
   p.log_base = log(a.rope_base);
   const int total = (a.d_c + kBox - 1) / kBox + (a.d_R + kBox - 1) / kBox;
   const int token_tiles = (a.T + kTokens - 1) / kTokens, kb = a.d_model / 64;
-  // Boxes per CTA and CTAs along K.
+  // Boxes per CTA and CTAs along K, by what was measured (us): a block of 64
+  // columns takes 0.22 or its bytes at 130 per ns, the exchange of the partial
+  // tile its bytes at 25 per ns, the rest 5.  At d_model = 7168 the model is
+  // within 10 % of the best and of the runners-up: 37 tokens 8.5 with (2 boxes,
+  // 8 CTAs) against 10.6 with (1, 4) and (6, 8); 1024 tokens 17.9 with (6, 4),
+  // 19.8 with (2, 2), 27.5 with (6, 2).
   int cs = 1;
   p.boxes = 1;
   double best = 0;
   for (int j = 1; j <= std::min(kMaxBoxes, total); ++j)
-    for (int c = 1; c <= kMaxCluster && c <= kb; c *= 2) {
-      const int ctas = (total + j - 1) / j * token_tiles * c;
-      const int waves = (ctas + a.sm_count - 1) / a.sm_count;
-      const double load = (double)((kb + c - 1) / c) * (p.x_rows * 128 + j * kBoxBytes) / 130.0;
-      const double reduce = (double)std::min(a.T, kTokens) * j * kBox * 4 / 100.0;
-      const double t = waves * (load + reduce + 3000);
+    for (int e = 0; e < kClusterSizes && (1 << e) <= kb; ++e) {
+      const int clusters = (total + j - 1) / j * token_tiles;
+      const int waves = (clusters + a.max_clusters[e] - 1) / a.max_clusters[e];
+      const double block = std::max(0.22, (p.x_rows * 128 + j * kBoxBytes) / 130e3);
+      const double t = waves * (((kb + (1 << e) - 1) >> e) * block +
+                                std::min(a.T, kTokens) * j * kBox * 4 / 25e3 + 5);
       if (best == 0 || t < best) {
         best = t;
         p.boxes = j;
-        cs = c;
+        cs = 1 << e;
       }
     }
   const uint32_t stage = p.x_rows * 128 + p.boxes * kBoxBytes;

@@ -219,12 +219,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, MLA_DEVFLAG_TIMEOUT));
 }
-__device__ __forceinline__ bool warp_wait2(uint32_t bar0, uint32_t par0, uint32_t bar1,
-                                           uint32_t par1, int* err) {
-  const bool a = mbar_wait(bar0, par0, err, MLA_DEVFLAG_TIMEOUT);
-  const bool b = mbar_wait(bar1, par1, err, MLA_DEVFLAG_TIMEOUT);
-  return __all_sync(0xffffffffu, a && b);
-}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_sm100_kernel(const __grid_constant__ Params p) {
@@ -465,15 +459,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // rows past the sequence end may hold anything; make them zero so
         // that 0-probability x garbage cannot turn into NaN in P . C
         uint8_t* tile = base + kOffKv + s * kStageBytes;
-        for (int r = max(rows_valid, 0); r < kTreeTile; ++r) {
-          if (lane < 8)
-            for (int kb = 0; kb < 4; ++kb)
-              *reinterpret_cast<uint4*>(tile + kb * kKvBlk + r * 128 + lane * 16) =
-                  make_uint4(0, 0, 0, 0);
-          if (lane < 4)
-            *reinterpret_cast<uint4*>(tile + 4 * kKvBlk + r * 64 + lane * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
+        // 16 bytes per lane: a row's 4 x 128 latent bytes, 8 rows' 64 RoPE bytes
+        for (int r = rows_valid; r < kTreeTile; ++r)
+          *reinterpret_cast<uint4*>(tile + (lane >> 3) * kKvBlk + r * 128 + (lane & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        for (int r = rows_valid + (lane >> 2); r < kTreeTile; r += 8)
+          *reinterpret_cast<uint4*>(tile + 4 * kKvBlk + r * 64 + (lane & 3) * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) signal_lead(KV_FULL + s, true, 4u, 9);
@@ -490,7 +481,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // only its own thread's MMAs, so a P . C whose P is ready never waits
     // behind an S being issued (issuing blocks while the tensor pipe's queue
     // is full) and vice versa.
-    if (leader) {
+    // One elected thread per warp does all of it, waits included: between two
+    // products no other lane has to be met again.
+    if (leader && elect_one()) {
       constexpr uint32_t kIdS = idesc_bf16(256, 128, false);
       constexpr uint32_t kIdPV = idesc_bf16(128, 256, true);
       TreeWalk walk;
@@ -509,58 +502,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // S for global tile g: 16 steps over the latent columns, 2 over RoPE
       auto issue_s = [&](int g, bool last) {
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t st = (g % kStages) * (kStageBytes >> 4);
-          const uint32_t dS = tmem + kTmemS + (g & 1) * 128;
+        const uint32_t st = (g % kStages) * (kStageBytes >> 4);
+        const uint32_t dS = tmem + kTmemS + (g & 1) * 128;
 #pragma unroll
-          for (int kc = 0; kc < 4; ++kc)
+        for (int kc = 0; kc < 4; ++kc)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16_ss_pair(dS, q_lat + kc * (kQBlk >> 4) + ks * 2,
-                               k_lat + st + kc * (kKvBlk >> 4) + ks * 2, kIdS, kc + ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ss_pair(dS, q_lat + kc * (kQBlk >> 4) + ks * 2,
+                             k_lat + st + kc * (kKvBlk >> 4) + ks * 2, kIdS, kc + ks > 0 ? 1u : 0u);
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-            umma_f16_ss_pair(dS, q_rope + ks * 2, k_rope + st + ks * 2, kIdS, 1u);
-          umma_commit_pair(bar(S_FULL + (g & 1)), kBothCtas);
-          if (last) umma_commit_pair(bar(Q_EMPTY), kBothCtas);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 2; ++ks)
+          umma_f16_ss_pair(dS, q_rope + ks * 2, k_rope + st + ks * 2, kIdS, 1u);
+        umma_commit_pair(bar(S_FULL + (g & 1)), kBothCtas);
+        if (last) umma_commit_pair(bar(Q_EMPTY), kBothCtas);
       };
       // O (+)= P . C for global tile g; `first` = first tile of its segment
       auto issue_pv = [&](int g, bool first) {
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t st = (g % kStages) * (kStageBytes >> 4);
-          // P tokens 0-31 sit in the stage's RoPE block (S is done with it),
-          // tokens 32-63 in the second-half ring
-          const uint64_t pa[2] = {k_rope + st, p_ring + (g & 1) * (kPHalf >> 4)};
+        const uint32_t st = (g % kStages) * (kStageBytes >> 4);
+        // P tokens 0-31 sit in the stage's RoPE block (S is done with it),
+        // tokens 32-63 in the second-half ring
+        const uint64_t pa[2] = {k_rope + st, p_ring + (g & 1) * (kPHalf >> 4)};
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk)
+        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 16 tokens per MMA
-              umma_f16_ss_pair(tmem + kTmemO + blk * 128, pa[kk >> 1] + (kk & 1) * 2,
-                               v_lat + st + 2 * blk * (kKvBlk >> 4) + kk * (2048 >> 4), kIdPV,
-                               (first && kk == 0) ? 0u : 1u);
-          umma_commit_pair(bar(KV_EMPTY + g % kStages), kBothCtas);
-          umma_commit_pair(bar(PV_DONE + (g & 1)), kBothCtas);
-        }
-        __syncwarp();
+          for (int kk = 0; kk < 4; ++kk)  // 16 tokens per MMA
+            umma_f16_ss_pair(tmem + kTmemO + blk * 128, pa[kk >> 1] + (kk & 1) * 2,
+                             v_lat + st + 2 * blk * (kKvBlk >> 4) + kk * (2048 >> 4), kIdPV,
+                             (first && kk == 0) ? 0u : 1u);
+        umma_commit_pair(bar(KV_EMPTY + g % kStages), kBothCtas);
+        umma_commit_pair(bar(PV_DONE + (g & 1)), kBothCtas);
       };
       // Fixed order per segment: S0 S1 S2, then P.C(j) S(j+3) for every tile
       // j, so S runs two tiles ahead of P.C and the softmax of tile j has
       // two S groups of tensor work to hide behind.  Each step polls only the
       // barriers it needs (a barrier test costs ~150 cycles; re-testing a
       // ready barrier is not free).
+      auto wait = [&](int b, uint32_t parity) {
+        return mbar_wait(bar(b), parity, p.err, MLA_DEVFLAG_TIMEOUT);
+      };
       const bool s_issuer = warp == kWarpMma;
       while (ok && walk.next(sg)) {
         const int n_t = sg.t1 - sg.t0;
         if (s_issuer) {
           // S(g) once its stage is loaded and its S buffer has been read
-          if (!(ok = warp_wait(bar(Q_FULL), seg_i & 1, p.err))) break;
+          if (!(ok = wait(Q_FULL, seg_i & 1))) break;
           for (int j = 0; ok && j < n_t; ++j) {
             const int g = g0 + j;
-            if (!(ok = warp_wait2(bar(KV_FULL + g % kStages), (g / kStages) & 1,
-                                  bar(S_EMPTY + (g & 1)), ((g >> 1) & 1) ^ 1, p.err)))
+            if (!(ok = wait(S_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1) &&
+                       wait(KV_FULL + g % kStages, (g / kStages) & 1)))
               break;
             issue_s(g, j == n_t - 1);
           }
@@ -568,10 +558,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // P . C(g) once P(g) is written
           for (int j = 0; ok && j < n_t; ++j) {
             const int g = g0 + j;
-            if (!(ok = warp_wait(bar(P_FULL + (g & 1)), (g >> 1) & 1, p.err))) break;
+            if (!(ok = wait(P_FULL + (g & 1), (g >> 1) & 1))) break;
             // the segment's first P . C overwrites O: every softmax warp of
             // both CTAs must have read the last segment's
-            if (j == 0 && seg_i > 0 && !(ok = warp_wait(bar(O_FREE), (seg_i - 1) & 1, p.err))) break;
+            if (j == 0 && seg_i > 0 && !(ok = wait(O_FREE, (seg_i - 1) & 1))) break;
             issue_pv(g, j == 0);
           }
         }
@@ -580,9 +570,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // every MMA issued by this thread has completed before TMEM is freed
       const int fin = s_issuer ? MMA_FINAL : MMA_FINAL_PV;
-      if (elect_one()) umma_commit_pair(bar(fin), 1);
-      warp_wait(bar(fin), 0, p.err);
+      umma_commit_pair(bar(fin), 1);
+      wait(fin, 0);
     }
+    __syncwarp();
   } else if (warp >= kWarpSoftmax0) {
     // ------------------------------------------------------------ softmax
     // Two groups of four warps take alternate tiles (group = g & 1, which is

@@ -17,9 +17,10 @@ constexpr int kTreeRows = 128;     // (token, head) rows of one row block
 // output of the last), in 64-token tiles.
 constexpr int kTreeSegTiles = 4;
 
-// Workspace of mla_decode_tree.  rec: 4 ints per chunk boundary (G + 1 of
-// them): sequence, row block and tile where the chunk starts, 0; the last one
-// is (B, 0, 0, 0).  up / cp: per-sequence prefix sums of the plan, used there
+// Workspace of mla_decode_tree.  rec: 8 ints per chunk boundary (G + 1 of
+// them): sequence, row block and tile where the chunk starts, 0, then that
+// sequence's first token, drafted tokens and length, 0; the last one is
+// (B, 0, ...).  up / cp: per-sequence prefix sums of the plan, used there
 // only when the batch is too large for shared memory.  part_u / part_lse: the
 // partial results of pieces of row blocks, 128 rows per slot: chunk c writes a
 // piece that continues a block into slot 2c and one that begins a block in

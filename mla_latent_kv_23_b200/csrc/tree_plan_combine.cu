@@ -3,8 +3,8 @@
 // plan (one block): validates every sequence, and cuts the line of all row
 // blocks' tiles into chunks.  Two cuts:
 //   * pieces: with no more row blocks than chunks, block v of t tiles gets
-//     1 + floor((chunks - blocks) t / (all tiles)) chunks of its own (at most
-//     t), so that no chunk holds two blocks; the sum stays within the chunks;
+//     1 + floor((chunks - blocks) t / (all tiles)) chunks of its own (at
+//     most one per two tiles, and one up to kWholeTiles), so that no chunk holds two blocks; the sum stays within the chunks;
 //   * line: every block takes kTreeSegTiles + t units (a chunk that enters one
 //     more block pays for its queries and its output), the line is cut into
 //     equal units, and a cut that would leave kSnap tiles or fewer of a block
@@ -32,6 +32,11 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSmemSeqs = 2048;  // batches up to this size keep the prefix sums on chip
 constexpr int kSnap = 2;
+// A block of up to four tiles is not cut into pieces, and pieces have two tiles
+// or more: a tile takes 1 us, partial results and their merge 2 to 4 (one block
+// of 2 tiles: 12.8 us whole, 14.1 cut; 4 tiles: 14.7 either way; 8 tiles: 18.7
+// whole, 15.3 in four pieces, 15.8 in eight).
+constexpr int kWholeTiles = 4;
 
 // Inclusive scan of one value per thread; *total gets the block's sum.
 __device__ long long block_scan(long long v, long long* warp_sums, long long* total) {
@@ -94,8 +99,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   // pieces of each of sequence i's blocks
   auto pieces = [&](const TreeSeq& s) -> int {
     if (s.blocks == 0) return 0;
+    if (s.tiles <= kWholeTiles) return 1;
     const long long n = 1 + (num_chunks - blocks_all) * s.tiles / tiles_all;
-    return n < s.tiles ? (int)n : s.tiles;
+    return (int)min(n, (long long)(s.tiles + 1) / 2);
   };
   if (fits) {
     long long chunks = 0;
@@ -118,6 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const bool cut_pieces = fits && longest_piece <= per + K;
   for (int c = threadIdx.x; c <= num_chunks; c += kPlanThreads) {
     int b = B, g = 0, t = 0;
+    TreeSeq first = {0, 0, 0, 0, 0, 0};
     if (cut_pieces ? c < cp[B] : c * per < units_all) {
       const long long x = cut_pieces ? c : c * per;
       int lo = 0, hi = B;  // the largest b that starts at or before x
@@ -142,8 +149,11 @@ __global__ void __launch_bounds__(kPlanThreads)
           ++g;  // past the sequence's last block: the walk goes on to the next sequence
         }
       }
+      first = s;
     }
-    *reinterpret_cast<int4*>(rec + 4 * c) = make_int4(b, g, t, 0);
+    int4* r = reinterpret_cast<int4*>(rec) + 2 * c;
+    r[0] = make_int4(b, g, t, 0);
+    r[1] = make_int4(first.row0, first.n, first.L, 0);
   }
 }
 
@@ -201,24 +211,23 @@ __global__ void __launch_bounds__(kCombineThreads)
       if (lane == 0 && lse_out != nullptr) lse_out[row] = -INFINITY;
     }
   }
-  const int4 start = *reinterpret_cast<const int4*>(rec + 4 * c);
-  const int4 end = *reinterpret_cast<const int4*>(rec + 4 * c + 4);
+  const int4* r = reinterpret_cast<const int4*>(rec);
+  const int4 start = r[2 * c], end = r[2 * c + 2], seq = r[2 * c + 3];
   if (end.z == 0) return;  // not cut inside a block
   if (start.x == end.x && start.y == end.y && start.z > 0) return;  // it began in an earlier chunk
   // the chunks after this one that also end inside the block
   int pieces = 2;
   for (int d0 = c + 2; d0 <= num_chunks; d0 += 32) {
     int4 e = make_int4(-1, 0, 0, 0);
-    if (d0 + lane <= num_chunks) e = *reinterpret_cast<const int4*>(rec + 4 * (d0 + lane));
+    if (d0 + lane <= num_chunks) e = r[2 * (d0 + lane)];
     const uint32_t same =
         __ballot_sync(0xffffffffu, e.x == end.x && e.y == end.y && e.z > 0);
     const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
     pieces += run;
     if (run < 32) break;
   }
-  const TreeSeq s = tree_seq(cu_q, seqlens, end.x, T, n_h, max_len);
   const int i = blockIdx.x * kCombineWarps + warp;  // row of the block
-  if (i >= min(kTreeRows, s.n * n_h - end.y * kTreeRows)) return;
+  if (i >= min(kTreeRows, seq.y * n_h - end.y * kTreeRows)) return;
   // slot of piece k: 2c + 1, then 2 (c + 1), 2 (c + 2), ...
   auto prow = [&](int k) -> size_t {
     return (size_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * kTreeRows + i;
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         }
       }
     }
-  const size_t row = (size_t)s.row0 * n_h + (size_t)end.y * kTreeRows + i;
+  const size_t row = (size_t)seq.x * n_h + (size_t)end.y * kTreeRows + i;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) store4<kOutBf16>(u_out, row * kDc + 4 * lane + 128 * j, acc[j]);
   if (lane == 0 && lse_out != nullptr) lse_out[row] = lse;
@@ -283,7 +292,7 @@ TreeWsLayout tree_ws_layout(int B, int d_c, int num_chunks) {
   TreeWsLayout L;
   size_t off = 0;
   L.rec = off;
-  off = up256(off + sizeof(int) * 4 * ((size_t)num_chunks + 1));
+  off = up256(off + sizeof(int) * 8 * ((size_t)num_chunks + 1));
   L.up = off;
   off = up256(off + sizeof(long long) * ((size_t)B + 1));
   L.cp = off;

@@ -27,6 +27,11 @@ struct TreeSeq {
   int flag;
 };
 
+__device__ __forceinline__ void tree_extent(TreeSeq& s, int n_h) {
+  s.blocks = (s.n * n_h + kTreeRows - 1) / kTreeRows;
+  s.tiles = (s.L - 1) / kTreeTile + 1;
+}
+
 __device__ __forceinline__ TreeSeq tree_seq(const int* __restrict__ cu_q,
                                             const int* __restrict__ seqlens, int b, int T, int n_h,
                                             long long max_len) {
@@ -44,12 +49,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const int* __restrict__ cu_q,
     s.n = end - s.row0;
   s.blocks = s.tiles = 0;
   if (s.n > 0) {
-    if (s.L < s.n || s.L > max_len) {
+    if (s.L < s.n || s.L > max_len)
       s.flag = MLA_DEVFLAG_BAD_SEQLEN;  // its rows get u = 0, lse = -inf
-    } else {
-      s.blocks = (s.n * n_h + kTreeRows - 1) / kTreeRows;
-      s.tiles = (s.L - 1) / kTreeTile + 1;
-    }
+    else
+      tree_extent(s, n_h);
   }
   return s;
 }
@@ -82,15 +85,21 @@ struct TreeWalk {
     n_h = heads;
     max_len = longest;
     chunk = chunk_id;
-    const int4 r0 = *reinterpret_cast<const int4*>(rec + 4 * chunk_id);
-    const int4 r1 = *reinterpret_cast<const int4*>(rec + 4 * chunk_id + 4);
+    const int4* r = reinterpret_cast<const int4*>(rec) + 2 * chunk_id;
+    const int4 r0 = r[0], s0 = r[1], r1 = r[2];  // independent: one memory round trip
     b = r0.x;
     g = r0.y;
     t = r0.z;
     be = r1.x;
     ge = r1.y;
     te = r1.z;
-    loaded = false;
+    // the first sequence comes with the record
+    seq.row0 = s0.x;
+    seq.n = s0.y;
+    seq.L = s0.z;
+    seq.flag = 0;
+    tree_extent(seq, n_h);
+    loaded = true;
   }
 
   __device__ __forceinline__ bool next(TreeSegment& s) {
