@@ -170,50 +170,67 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
     if (job < a.B) {
       const int b = (int)job;
       const Request r = request(a, b);
+      const int t0 = cu[b];
+      const bool tree = trees && t0 < total && r.n <= kTreeMaxNodes;
+      // tokens lane and lane + 32 of a tree: their parents are on their way
+      // while the pages are looked up
+      int up[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        up[h] = tree && i < r.n && t0 + i < total ? a.parents[t0 + i] : -1;
+      }
       const long long first = (long long)used + pg[b];
       for (int k = r.have + lane; k < r.want; k += 32) {
         const int page = page_at(a, b, k, r.have, first, flags);
         a.block_table[(size_t)b * a.max_pages + k] = page;
       }
-      if (!trees) continue;
-      const int t0 = cu[b];
-      if (t0 >= total) continue;
-      if (r.n > kTreeMaxNodes) {  // a prompt: no branches
+      if (!trees || t0 >= total) continue;
+      if (!tree) {  // a prompt: no branches
         for (int i = lane; i < min(r.n, total - t0); i += 32) a.tree_mask[t0 + i] = 0;
         continue;
       }
-      // tokens lane and lane + 32: branches of 1, 2, 4 ... 64 tokens, joined
-      // with the branch that ends where they begin.  A token without a parent
-      // points at itself.
-      unsigned long long m[2];
-      int up[2];
+      // branches of 1, 2, 4 ... 64 tokens, joined with the branch that ends
+      // where they begin.  A token without a parent points at itself.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = lane + 32 * h;
-        int parent = i < r.n && t0 + i < total ? a.parents[t0 + i] : -1;
-        if (parent < -1 || parent >= i) {
+        if (up[h] < -1 || up[h] >= i) {
           flags |= MLA_DEVFLAG_BAD_TREE;
-          parent = -1;
+          up[h] = -1;
         }
-        up[h] = parent < 0 ? i : parent;
-        m[h] = 1ull << i;
+        if (up[h] < 0) up[h] = i;
       }
-      for (int d = 1; d < r.n; d <<= 1) {
-        unsigned long long jm[2];
-        int ju[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const unsigned long long lo = __shfl_sync(0xffffffffu, m[0], up[h] & 31);
-          const unsigned long long hi = __shfl_sync(0xffffffffu, m[1], up[h] & 31);
-          const int ulo = __shfl_sync(0xffffffffu, up[0], up[h] & 31);
-          const int uhi = __shfl_sync(0xffffffffu, up[1], up[h] & 31);
-          jm[h] = up[h] < 32 ? lo : hi;
-          ju[h] = up[h] < 32 ? ulo : uhi;
+      unsigned long long m[2];
+      if (r.n <= 32) {
+        uint32_t mask = 1u << lane;
+        int u = up[0];
+        for (int d = 1; d < r.n; d <<= 1) {
+          mask |= __shfl_sync(0xffffffffu, mask, u);
+          u = __shfl_sync(0xffffffffu, u, u);
         }
+        m[0] = mask;
+        m[1] = 0;
+      } else {
+        m[0] = 1ull << lane;
+        m[1] = 1ull << (lane + 32);
+        for (int d = 1; d < r.n; d <<= 1) {
+          unsigned long long jm[2];
+          int ju[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          m[h] |= jm[h];
-          up[h] = ju[h];
+          for (int h = 0; h < 2; ++h) {
+            const unsigned long long lo = __shfl_sync(0xffffffffu, m[0], up[h] & 31);
+            const unsigned long long hi = __shfl_sync(0xffffffffu, m[1], up[h] & 31);
+            const int ulo = __shfl_sync(0xffffffffu, up[0], up[h] & 31);
+            const int uhi = __shfl_sync(0xffffffffu, up[1], up[h] & 31);
+            jm[h] = up[h] < 32 ? lo : hi;
+            ju[h] = up[h] < 32 ? ulo : uhi;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            m[h] |= jm[h];
+            up[h] = ju[h];
+          }
         }
       }
 #pragma unroll
