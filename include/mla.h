@@ -484,8 +484,11 @@ mla_status mla_build_tables(const mla_tables_params* p, void* stream);
  *
  * Softmax statistics, sums and the partial results of rows split over KV chunks
  * are fp32; the softmax weights are rounded to bf16 for the product with C, and
- * u is normalised by the sum of the rounded weights.
- * Supported: bf16, d_c = 512, d_R = 64, n_h <= 128.  All pointers 16-byte
+ * u is normalised by the sum of the rounded weights (fp32 tensors enter both
+ * products as tf32, and so do the weights).
+ * Supported, for n_h <= 128: bf16 with d_c = 512 and d_R = 64, or with d_c a
+ * multiple of 64 and d_c + d_R <= 256; fp32 (u fp32) with d_c a multiple of 32
+ * and d_c + d_R <= 128.  All pointers 16-byte
  * aligned; the workspace is 256-byte aligned scratch that keeps no state.
  * Calls that share a workspace must be ordered on the GPU.
  */

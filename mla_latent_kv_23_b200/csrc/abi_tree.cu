@@ -6,6 +6,7 @@
 
 #include "abi_common.h"
 #include "append_slots.h"
+#include "internal.h"
 #include "mla.h"
 #include "tables.h"
 #include "tree.h"
@@ -49,9 +50,16 @@ mla_status validate_tree(const mla_tree_params* p) {
   return MLA_OK;
 }
 
-bool tree_v3(const mla_tree_params* p, const DeviceInfo* d) {
-  return d->cc_major == 10 && g_encode != nullptr && d->tree_clusters > 0 &&
-         p->dtype == MLA_DTYPE_BF16 && p->d_c == 512 && p->d_R == 64;
+// The attend kernels: paired CTAs for the DeepSeek-V3 shape (bf16, d_c = 512,
+// d_R = 64), one CTA for the small latent widths.
+enum class TreeKernel { kNone, kV3, kSmall };
+
+TreeKernel tree_kernel(const mla_tree_params* p, const DeviceInfo* d) {
+  if (d->cc_major != 10 || g_encode == nullptr) return TreeKernel::kNone;
+  const bool bf16 = p->dtype == MLA_DTYPE_BF16;
+  if (bf16 && p->d_c == 512 && p->d_R == 64 && d->tree_clusters > 0) return TreeKernel::kV3;
+  if (d->small_tc && decode_small_sm100_supported(bf16, p->d_c, p->d_R)) return TreeKernel::kSmall;
+  return TreeKernel::kNone;
 }
 
 // One chunk per resident cluster, but no more than the batch can have tiles by
@@ -62,7 +70,28 @@ int tree_chunks(const mla_tree_params* p, const DeviceInfo* d) {
   const long long blocks = p->B + (long long)p->T * p->n_h / kTreeRows;
   const long long tiles = (long long)p->max_pages_per_seq * p->page_size / kTreeTile;
   const long long most = blocks * tiles;
-  return most < d->tree_clusters ? (int)(most < 1 ? 1 : most) : d->tree_clusters;
+  const int resident = tree_kernel(p, d) == TreeKernel::kV3 ? d->tree_clusters : d->sm_count;
+  return most < resident ? (int)(most < 1 ? 1 : most) : resident;
+}
+
+mla_status plan_and_attend_small(const mla_tree_params* p, const TreeArgs& a, cudaStream_t s) {
+  const cuuint64_t es = a.bf16 ? 2 : 4, W = (cuuint64_t)p->d_c + p->d_R;
+  const auto type = a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const cuuint64_t qdims[2] = {W, (cuuint64_t)p->T * p->n_h};
+  const cuuint64_t kdims[2] = {W, (cuuint64_t)p->num_pages * p->page_size};
+  const cuuint64_t strides[1] = {W * es};
+  const cuuint32_t qbox[2] = {static_cast<cuuint32_t>(128 / es), 128};
+  const cuuint32_t kbox[2] = {static_cast<cuuint32_t>(128 / es), kTreeTile};
+  CUtensorMap q, kv, kv_pv;
+  memset(&kv_pv, 0, sizeof(kv_pv));
+  if (!encode(&q, type, 2, p->q, qdims, strides, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&kv, type, 2, p->kv_cache, kdims, strides, kbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      // an MN-major tf32 operand: 128-byte swizzle of 32-byte atoms
+      (!a.bf16 && !encode(&kv_pv, type, 2, p->kv_cache, kdims, strides, kbox,
+                          CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B)))
+    return MLA_ERR_CUDA;
+  const mla_status st = cuda_status(launch_tree_plan(a, s));
+  return st != MLA_OK ? st : cuda_status(launch_tree_small_sm100(a, q, kv, kv_pv, s));
 }
 
 mla_status encode_tree(TreeMaps* m, const mla_tree_params* p, const TreeArgs& a) {
@@ -123,7 +152,7 @@ mla_status mla_decode_tree_workspace_size(const mla_tree_params* p, size_t* byte
   if (st != MLA_OK) return st;
   const DeviceInfo* d = nullptr;
   if ((st = device_info(&d)) != MLA_OK) return st;
-  if (!tree_v3(p, d)) return MLA_ERR_UNSUPPORTED;
+  if (tree_kernel(p, d) == TreeKernel::kNone) return MLA_ERR_UNSUPPORTED;
   *bytes = tree_ws_layout(p->B, p->d_c, tree_chunks(p, d)).total;
   return MLA_OK;
 }
@@ -134,7 +163,7 @@ mla_status mla_decode_tree(const mla_tree_params* p, void* workspace, size_t wor
   if (st != MLA_OK || p->B == 0 || p->T == 0) return st;
   const DeviceInfo* d = nullptr;
   if ((st = device_info(&d)) != MLA_OK) return st;
-  if (!tree_v3(p, d)) return MLA_ERR_UNSUPPORTED;
+  if (tree_kernel(p, d) == TreeKernel::kNone) return MLA_ERR_UNSUPPORTED;
   const int G = tree_chunks(p, d);
   const TreeWsLayout L = tree_ws_layout(p->B, p->d_c, G);
   if (workspace_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
@@ -169,10 +198,14 @@ mla_status mla_decode_tree(const mla_tree_params* p, void* workspace, size_t wor
   a.bf16 = p->dtype == MLA_DTYPE_BF16;
   a.out_f32 = p->u_fp32 != 0 || p->dtype == MLA_DTYPE_FP32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  TreeMaps maps;
-  if ((st = encode_tree(&maps, p, a)) != MLA_OK) return st;
-  if ((st = cuda_status(launch_tree_plan(a, s))) != MLA_OK) return st;
-  if ((st = cuda_status(launch_tree_sm100(a, maps, s))) != MLA_OK) return st;
+  if (tree_kernel(p, d) == TreeKernel::kV3) {
+    TreeMaps maps;
+    if ((st = encode_tree(&maps, p, a)) != MLA_OK) return st;
+    if ((st = cuda_status(launch_tree_plan(a, s))) != MLA_OK) return st;
+    if ((st = cuda_status(launch_tree_sm100(a, maps, s))) != MLA_OK) return st;
+  } else if ((st = plan_and_attend_small(p, a, s)) != MLA_OK) {
+    return st;
+  }
   return cuda_status(launch_tree_combine(a, s));
 }
 

@@ -38,12 +38,22 @@
 // group and every query row as the MMA rows, so a tile of the group's cache
 // is read once for all s_q rows (the MTP case, s_q = 2).  S is taken over
 // [K^C_g || k^R] and P . V over V_g, loaded into the stage's value region.
+//
+// And it runs mla_decode_tree for these widths: the MMA rows are a block of 128
+// of a sequence's flat (token, head) rows, a row sees the context and the
+// drafted tokens of its mask word, and what non-finite values a drafted token's
+// cache row holds is cleared before P . C (rows that see the token get NaN by
+// their weight; the others must not meet 0 x NaN).
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "schedule.cuh"
 #include "sm100_ptx.cuh"
+#include "tree.h"
+#include "tree_schedule.cuh"
 
 namespace mla {
 namespace {
@@ -96,6 +106,12 @@ struct Params {
   float scale_log2;    // softmax_scale * log2(e)
   // GQA path: groups, heads per group, key / value / RoPE blocks
   int n_g, hpg, d_h, d_v, nbk, nbr, nbv;
+  // trees: chunk records, prefix sums, mask words, packed tokens (q_map: the
+  // flat rows [T n_h, W], box (one 128-byte block) x 128)
+  const int* rec;
+  const int* cu_q;
+  const unsigned long long* mask;
+  int T;
 };
 
 template <bool kTf32, bool kGqa>
@@ -125,7 +141,7 @@ __device__ __forceinline__ float to_tf32(float x) {
   return __uint_as_float(r);
 }
 
-template <bool kTf32, bool kGqa>
+template <bool kTf32, bool kGqa, bool kTree = false>
 __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const __grid_constant__ Params p) {
   using Lay = Layout<kTf32, kGqa>;
   constexpr int kStages = Lay::kStages;
@@ -135,9 +151,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // MLA: (chunk, query row); GQA: (chunk, group) with every query row
-  const int chunk = blockIdx.x / (kGqa ? p.n_g : p.s_q);
-  const int qrow = kGqa ? 0 : blockIdx.x % p.s_q;
+  // MLA: (chunk, query row); GQA: (chunk, group) with every query row; trees: chunk
+  const int chunk = blockIdx.x / (kTree ? 1 : kGqa ? p.n_g : p.s_q);
+  const int qrow = kTree || kGqa ? 0 : blockIdx.x % p.s_q;
+  using Walk = std::conditional_t<kTree, TreeWalk, ChunkWalk>;
+  using Seg = std::conditional_t<kTree, TreeSegment, Segment>;
+  auto start = [&](Walk& walk) {
+    if constexpr (kTree)
+      walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, (long long)p.max_pages * p.page_size, chunk);
+    else
+      walk.init(p.tile_prefix, p.chunk_t, p.chunk_b, p.header, p.B, chunk);
+  };
+  auto length = [&](const Seg& sg) {
+    if constexpr (kTree) return sg.seq.L; else return p.seqlens[sg.b];
+  };
   const int grp = kGqa ? blockIdx.x % p.n_g : 0;
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kOffBar + 8u * i; };
   const int nb = p.blocks;
@@ -188,9 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
       prefetch_tmap(&p.kv_map);
       if (kTf32) prefetch_tmap(&p.kv_pv_map);
       if (kGqa) prefetch_tmap(&p.kr_map);
-      ChunkWalk walk;
-      walk.init(p.tile_prefix, p.chunk_t, p.chunk_b, p.header, p.B, chunk);
-      Segment sg;
+      Walk walk;
+      start(walk);
+      Seg sg;
       int g = 0, seg_i = 0;
       bool ok = true;
       while (ok && walk.next(sg)) {
@@ -199,7 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
           break;
         mbar_arrive_expect_tx(bar(Q_FULL), nb * q_rows * 128);
         for (int k = 0; k < nb; ++k) {
-          if (kGqa)  // rows (r, h): query row r, head h of the group
+          if constexpr (kTree)  // flat rows; those past the block's last are not written
+            tma_load_2d(sbase + Lay::kOffQ + k * kQBlkBytes, &p.q_map, bar(Q_FULL), k * Lay::kCols,
+                        sg.first);
+          else if (kGqa)  // rows (r, h): query row r, head h of the group
             tma_load_3d(sbase + Lay::kOffQ + k * kQBlkBytes, &p.q_map, bar(Q_FULL), k * Lay::kCols,
                         grp * p.hpg, sg.b * p.s_q);
           else
@@ -249,9 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
     const uint32_t idS = kTf32 ? idesc_tf32(kRows, kTileTokens, false)
                                : idesc_bf16(kRows, kTileTokens, false);
     const uint32_t idPV = kTf32 ? idesc_tf32(kRows, d_c, true) : idesc_bf16(kRows, d_c, true);
-    ChunkWalk walk;
-    walk.init(p.tile_prefix, p.chunk_t, p.chunk_b, p.header, p.B, chunk);
-    Segment sg;
+    Walk walk;
+    start(walk);
+    Seg sg;
     int g0 = 0, seg_i = 0;
     bool ok = true;
     auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
     };
     while (ok && walk.next(sg)) {
       const int n_t = sg.t1 - sg.t0;
-      const int L = p.seqlens[sg.b];
+      const int L = length(sg);
       bool wait_ok = true;
       if (lane == 0) wait_ok = mbar_wait(bar(Q_FULL), seg_i & 1, p.err, MLA_DEVFLAG_TIMEOUT);
       if (!(ok = __shfl_sync(0xffffffffu, wait_ok, 0))) break;
@@ -361,12 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
     const int row = 32 * q4 + lane;  // MMA row: head (MLA) or (query row, head of the group) (GQA)
     const int r_row = kGqa ? row / p.hpg : qrow;                 // query row
     const int head = kGqa ? grp * p.hpg + row % p.hpg : row;
-    const bool live = kGqa ? row < p.hpg * p.s_q : row < p.n_h;
+    bool live = kGqa ? row < p.hpg * p.s_q : row < p.n_h;
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const float c_log2 = p.scale_log2;
-    ChunkWalk walk;
-    walk.init(p.tile_prefix, p.chunk_t, p.chunk_b, p.header, p.B, chunk);
-    Segment sg;
+    Walk walk;
+    start(walk);
+    Seg sg;
     int g = 0;
     bool ok = true;
     auto wwait = [&](uint32_t b, uint32_t par) -> bool {
@@ -375,8 +405,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
       return __shfl_sync(0xffffffffu, r, 0);
     };
     while (ok && walk.next(sg)) {
-      const int L = p.seqlens[sg.b];
+      const int L = length(sg);
       const int L_eff = L - p.s_q + 1 + r_row;
+      // trees: the position of the first drafted token, and which this row sees
+      int P0 = 0;
+      unsigned long long seen = 0;
+      if constexpr (kTree) {
+        P0 = L - sg.seq.n;
+        live = row < sg.rows;
+        if (live) seen = p.mask[sg.seq.row0 + (sg.g * kTreeRows + row) / p.n_h];
+        if (sg.seq.n < 64) seen &= (1ull << sg.seq.n) - 1;
+      }
       const int n_t = sg.t1 - sg.t0;
       float m = -INFINITY, l = 0.f, l_exact = 0.f;
       for (int j = 0; j < n_t; ++j, ++g) {
@@ -397,7 +436,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S_EMPTY + (g & 1)));
-        const int nv = L_eff - (sg.t0 + j) * kTileTokens;
+        const int tok0 = (sg.t0 + j) * kTileTokens;
+        unsigned long long clear = 0;  // tokens whose non-finite values must not meet P . C
+        if constexpr (kTree) {
+          if (tok0 + kTileTokens > P0) {
+            // bit k = position tok0 + k: the context, then the drafted tokens
+            const int sh = tok0 - P0;  // > -64; at most n - 1
+            const unsigned long long vis = sh >= 0 ? seen >> sh : (seen << -sh) | ((1ull << -sh) - 1);
+            uint32_t bad[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+              // (rows past the sequence's end are zero: their scores are finite)
+              if (!(fabsf(s[k]) <= 3.402823466e38f)) bad[k >> 5] |= 1u << (k & 31);
+              if (!((vis >> k) & 1)) s[k] = -INFINITY;
+            }
+            // a non-finite cache row makes every row's score so: one warp finds it
+            if (q4 == 0 && __any_sync(0xffffffffu, (bad[0] | bad[1]) != 0))
+              clear = __reduce_or_sync(0xffffffffu, bad[0]) |
+                      (static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, bad[1])) << 32);
+          }
+        }
+        const int nv = kTree ? kTileTokens : L_eff - tok0;
         float tmax = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 64; ++k) {
@@ -471,6 +530,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
             st_shared_v4(prow + ((static_cast<uint32_t>(k) ^ sw) << 4), w[0], w[1], w[2], w[3]);
           }
         }
+        if constexpr (kTree) {
+          // (uniform in the warp) S of this tile is done, its P . C waits for
+          // this warp: 16 bytes per lane of the P . C operand's rows
+          uint8_t* tile = base + Lay::kOffKv + (g % kStages) * Lay::kStageBytes +
+                          (kTf32 ? Lay::kPvCopy : 0) + (lane >> 3) * kKvBlkBytes + (lane & 7) * 16;
+          while (clear != 0 && (lane >> 3) * Lay::kCols < d_c) {
+            const int k = __ffsll(clear) - 1;
+            clear &= clear - 1;
+            uint4 v = *reinterpret_cast<uint4*>(tile + k * 128);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= kTf32 ? 0u : 0xffffu;
+              if (!kTf32 && (w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+            }
+            *reinterpret_cast<uint4*>(tile + k * 128) = v;
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -480,9 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
       // ---- epilogue: u = O / l for this row
       if (!(ok = wwait(bar(PV_DONE + ((g - 1) & 1)), ((g - 1) >> 1) & 1))) break;
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const size_t orow = sg.whole ? (size_t)(sg.b * p.s_q + r_row) * p.n_h + head
-                                   : ((size_t)(p.split_base[sg.b] + sg.part) * p.s_q + r_row) * p.n_h + head;
+      // (trees: a NaN sum, of non-finite scores, stays)
+      const float inv = (kTree ? l != 0.f : l > 0.f) ? 1.f / l : 0.f;
+      size_t orow;
+      if constexpr (kTree)
+        orow = sg.whole ? (size_t)sg.first + row : (size_t)sg.slot * kTreeRows + row;
+      else
+        orow = sg.whole ? (size_t)(sg.b * p.s_q + r_row) * p.n_h + head
+                        : ((size_t)(p.split_base[sg.b] + sg.part) * p.s_q + r_row) * p.n_h + head;
       for (int c0 = 0; c0 < d_c; c0 += 32) {
         float o[32];
         tmem_ld32(tmem + lane_base + kTmemO + c0, o);
@@ -509,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
         }
       }
       if (live) {
-        const float lse = l_exact > 0.f ? (m + log2f(l_exact)) * 0.69314718055994531f : -INFINITY;
+        const float lse = (kTree ? l_exact != 0.f : l_exact > 0.f)
+                              ? (m + log2f(l_exact)) * 0.69314718055994531f : -INFINITY;
         if (sg.whole) {
           if (p.lse != nullptr) p.lse[orow] = lse;
         } else {
@@ -548,7 +631,13 @@ int decode_small_sm100_prepare() {
                            (int)Layout<false, false>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(decode_small_sm100_kernel<false, true>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Layout<false, true>::kSmem) != cudaSuccess) {
+                           (int)Layout<false, true>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(decode_small_sm100_kernel<true, false, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Layout<true, false>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(decode_small_sm100_kernel<false, false, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Layout<false, false>::kSmem) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -647,6 +736,49 @@ cudaError_t launch_decode_gqa_sm100(const DecodeArgs& a, const GqaShape& gs, con
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, decode_small_sm100_kernel<false, true>, p);
+}
+
+cudaError_t launch_tree_small_sm100(const TreeArgs& a, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                                    const CUtensorMap& kv_pv_map, cudaStream_t s) {
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.q_map = q_map;
+  p.kv_map = kv_map;
+  p.kv_pv_map = kv_pv_map;
+  p.block_table = a.block_table;
+  p.seqlens = a.seqlens;
+  p.rec = a.rec;
+  p.cu_q = a.cu_q;
+  p.mask = a.mask;
+  p.T = a.T;
+  p.u = a.u;
+  p.lse = a.lse;
+  p.part_u = a.part_u;
+  p.part_lse = a.part_lse;
+  p.err = a.err;
+  p.B = a.B;
+  p.s_q = 1;
+  p.n_h = a.n_h;
+  p.d_c = a.d_c;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.num_pages = a.num_pages;
+  const int cols = a.bf16 ? 64 : 32;
+  p.blocks = (a.d_c + a.d_R + cols - 1) / cols;
+  p.out_f32 = a.out_f32 ? 1 : 0;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_chunks, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = a.bf16 ? Layout<false, false>::kSmem : Layout<true, false>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.bf16 ? cudaLaunchKernelEx(&cfg, decode_small_sm100_kernel<false, false, true>, p)
+                : cudaLaunchKernelEx(&cfg, decode_small_sm100_kernel<true, false, true>, p);
 }
 
 }  // namespace mla

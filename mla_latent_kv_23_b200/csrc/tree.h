@@ -69,4 +69,11 @@ struct TreeMaps {
 int tree_sm100_prepare();  // co-resident clusters, 0 if the kernel cannot run
 cudaError_t launch_tree_sm100(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);
 
+// The small-latent attend kernel (bf16 or fp32; decode_small_sm100_supported
+// says which widths).  q_map: the flat rows [T n_h, d_c + d_R], box 128 bytes x
+// 128 rows; kv_map: the cache, box 128 bytes x 64 rows, 128-byte swizzle;
+// kv_pv_map (fp32): the cache with 128-byte swizzle of 32-byte atoms.
+cudaError_t launch_tree_small_sm100(const TreeArgs& a, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                                    const CUtensorMap& kv_pv_map, cudaStream_t s);
+
 }  // namespace mla

@@ -185,20 +185,21 @@ __device__ __forceinline__ void store4(void* u, size_t at, float4 v) {
 }
 
 // Grid (16, chunks): 8 rows of the block that begins in chunk y and is cut at
-// its end.  One warp per row; lane l owns columns 4 l + 128 k.
-template <bool kOutBf16, int kDc>
+// its end.  One warp per row; lane l owns columns 4 l + 128 j, j < kVecs, below
+// d_c.
+template <bool kOutBf16, int kVecs>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const int* __restrict__ rec, const int* __restrict__ cu_q,
                         const int* __restrict__ seqlens, const float* __restrict__ part_u,
                         const float* __restrict__ part_lse, void* __restrict__ u_out,
-                        float* __restrict__ lse_out, int B, int T, int n_h, long long max_len,
-                        int num_chunks) {
-  constexpr int kVecs = kDc / 128;
+                        float* __restrict__ lse_out, int B, int T, int n_h, int d_c,
+                        long long max_len, int num_chunks) {
   constexpr int kGroup = 4;  // partial rows requested at a time
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.y;
+  auto mine = [&](int j) { return 4 * lane + 128 * j < d_c; };
   // sequences whose length is out of range
   for (long long b = (long long)c * gridDim.x + blockIdx.x; b < B; b += (long long)gridDim.x * gridDim.y) {
     const TreeSeq s = tree_seq(cu_q, seqlens, (int)b, T, n_h, max_len);
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     for (int r = warp; r < s.n * n_h; r += kCombineWarps) {
       const size_t row = (size_t)s.row0 * n_h + r;
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-        store4<kOutBf16>(u_out, row * kDc + 4 * lane + 128 * k, make_float4(0.f, 0.f, 0.f, 0.f));
+      for (int j = 0; j < kVecs; ++j)
+        if (mine(j)) store4<kOutBf16>(u_out, row * d_c + 4 * lane + 128 * j, make_float4(0.f, 0.f, 0.f, 0.f));
       if (lane == 0 && lse_out != nullptr) lse_out[row] = -INFINITY;
     }
   }
@@ -237,9 +238,10 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
     for (int k = 0; k < kGroup; ++k)
       if (k0 + k < pieces) {
-        const float* src = part_u + prow(k0 + k) * kDc + 4 * lane;
+        const float* src = part_u + prow(k0 + k) * d_c + 4 * lane;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) v[k][j] = *reinterpret_cast<const float4*>(src + 128 * j);
+        for (int j = 0; j < kVecs; ++j)
+          if (mine(j)) v[k][j] = *reinterpret_cast<const float4*>(src + 128 * j);
       }
   };
   // the first partial rows are requested together with the statistics
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   const size_t row = (size_t)seq.x * n_h + (size_t)end.y * kTreeRows + i;
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) store4<kOutBf16>(u_out, row * kDc + 4 * lane + 128 * j, acc[j]);
+  for (int j = 0; j < kVecs; ++j)
+    if (mine(j)) store4<kOutBf16>(u_out, row * d_c + 4 * lane + 128 * j, acc[j]);
   if (lane == 0 && lse_out != nullptr) lse_out[row] = lse;
 }
 
@@ -325,9 +328,10 @@ cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s) {
   auto go = [&](auto kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, (const int*)a.rec, a.cu_q, a.seqlens,
                               (const float*)a.part_u, (const float*)a.part_lse, a.u, a.lse, a.B,
-                              a.T, a.n_h, (long long)a.max_pages * a.page_size, a.num_chunks);
+                              a.T, a.n_h, a.d_c, (long long)a.max_pages * a.page_size, a.num_chunks);
   };
-  return a.out_f32 ? go(tree_combine_kernel<false, 512>) : go(tree_combine_kernel<true, 512>);
+  if (a.d_c <= 256) return a.out_f32 ? go(tree_combine_kernel<false, 2>) : go(tree_combine_kernel<true, 2>);
+  return a.out_f32 ? go(tree_combine_kernel<false, 4>) : go(tree_combine_kernel<true, 4>);
 }
 
 }  // namespace mla

@@ -15,11 +15,12 @@ D_C, D_R, W = 512, 64, 576
 SCALE = 1 / math.sqrt(192.0)
 
 
-def draw(sizes, lens, n_h, page=64, seed=0, masks="tree", spare_rows=3):
+def draw(sizes, lens, n_h, page=64, seed=0, masks="tree", spare_rows=3, width=(D_C, D_R), dtype=torch.bfloat16):
     """Inputs of a batch: `sizes` drafted tokens as the last of `lens` cached
     ones, over a shuffled pool whose unused rows hold NaN."""
     g = torch.Generator().manual_seed(seed)
     rng = np.random.default_rng(seed)
+    W = sum(width)
     need = [-(-n // page) for n in lens]
     pool = sum(need) + 2
     order = rng.permutation(pool).astype(np.int32)
@@ -51,7 +52,7 @@ def draw(sizes, lens, n_h, page=64, seed=0, masks="tree", spare_rows=3):
     q = torch.randn((T, n_h, W), generator=g)
     q[sum(sizes):] = float("nan")
     dev = "cuda"
-    return dict(q=q.to(torch.bfloat16).to(dev), cache=cache.to(torch.bfloat16).to(dev),
+    return dict(q=q.to(dtype).to(dev), cache=cache.to(dtype).to(dev), d_c=width[0],
                 table=torch.from_numpy(table).to(dev), lens=torch.tensor(lens, dtype=torch.int32, device=dev),
                 cu=torch.from_numpy(cu).to(dev), mask=torch.from_numpy(mask.view(np.int64)).to(dev), page=page,
                 sizes=sizes, n_h=n_h)
@@ -67,6 +68,10 @@ def reference(inp):
     enter its sums."""
     out = {}
     cu, lens, masks = inp["cu"].tolist(), inp["lens"].tolist(), inp["mask"].tolist()
+    d_c = inp.get("d_c", D_C)
+    # fp32 tensors enter the products as tf32, which may cut them: 2^-10
+    cut = 2.0 ** -10 if inp["q"].dtype == torch.float32 else 0.0
+    weight = 2.0 ** -11 if inp["q"].dtype == torch.float32 else 2.0 ** -8
     for b, n in enumerate(inp["sizes"]):
         if n == 0:
             continue
@@ -79,22 +84,22 @@ def reference(inp):
             kv = kv_all[keep]
             q = inp["q"][t].double()
             if len(kv) == 0:
-                z = torch.zeros((inp["n_h"], D_C), dtype=torch.float64, device="cuda")
+                z = torch.zeros((inp["n_h"], d_c), dtype=torch.float64, device="cuda")
                 out[t] = (z, z[:, 0] - math.inf, z + 1e-30, z[:, 0])
                 continue
             s = q @ kv.T * SCALE
             lse = torch.logsumexp(s, -1)
             a = torch.exp(s - lse[:, None])
-            u, abs_c = a @ kv[:, :D_C], a @ kv[:, :D_C].abs()
-            # A score is a sum of 576 products in fp32: off by at most 576
-            # half-steps of the sum of their sizes.  A weight moves by that
-            # (relatively) and by its rounding to bf16, 2^-8; u, normalised by
-            # the rounded weights, by (weight's) (abs_c + |u|), to first order;
+            u, abs_c = a @ kv[:, :d_c], a @ kv[:, :d_c].abs()
+            # A score is a sum of W products in fp32: off by at most W half-steps
+            # of the sum of their sizes, and by what its operands are cut.  A
+            # weight moves by that (relatively) and by its rounding; u, normalised
+            # by the rounded weights, by (weight's) (abs_c + |u|), to first order;
             # 1.02 covers the second.  Sums over L tokens in fp32 add L
             # half-steps, exp2 and log2 a few.
-            e = (q.abs() @ kv.abs().T * SCALE).amax(-1) * 576 * 2.0 ** -24
+            e = (q.abs() @ kv.abs().T * SCALE).amax(-1) * (q.shape[1] * 2.0 ** -24 + 2 * cut + cut * cut)
             tok = (len(kv) + 64) * 2.0 ** -24
-            du = 1.02 * (2.0 ** -8 + e + tok)[:, None] * (abs_c + u.abs())
+            du = 1.02 * (weight + e + tok)[:, None] * (abs_c + u.abs()) + cut * abs_c
             dl = e + tok + 2.0 ** -22 * (lse.abs() + s.abs().amax(-1) + 1)
             out[t] = (u, lse, du, dl)
     return out
@@ -117,10 +122,11 @@ def check(inp, u, lse):
 
 
 def run(inp, splits=0, u_dtype=torch.bfloat16, with_lse=True):
-    u = torch.full((inp["q"].shape[0], inp["n_h"], D_C), -7.0, dtype=u_dtype, device="cuda")
+    d_c = inp["d_c"]
+    u = torch.full((inp["q"].shape[0], inp["n_h"], d_c), -7.0, dtype=u_dtype, device="cuda")
     lse = torch.full(u.shape[:2], -7.0, device="cuda") if with_lse else None
     p = mla.tree_params(inp["q"], inp["cache"], inp["table"], inp["lens"], inp["cu"], inp["mask"], u, lse,
-                        inp["page"], D_R, SCALE, splits)
+                        inp["page"], inp["q"].shape[2] - d_c, SCALE, splits)
     ws = torch.full((mla.mla_decode_tree_workspace_size(p),), 255, dtype=torch.uint8, device="cuda")
     mla.mla_decode_tree(p, ws)
     return u, lse
@@ -323,3 +329,52 @@ def test_repeats_bit_for_bit():
     for _ in range(3):
         again = run(inp)
         assert torch.equal(first[0][:57], again[0][:57]) and torch.equal(first[1][:57], again[1][:57])
+
+
+@pytest.mark.parametrize("dtype,d_c,d_R", [(torch.bfloat16, 64, 16), (torch.bfloat16, 192, 64), (torch.bfloat16, 256, 0),
+                                           (torch.float32, 64, 16), (torch.float32, 96, 32)])
+@pytest.mark.parametrize("splits", [0, 3])
+@pytest.mark.parametrize("n_h,sizes,lens,masks", [
+    (8, (1, 0, 16, 33), (1, 50, 129, 1000), "tree"), (20, (7, 64), (64, 300), "any"), (128, (2, 1), (65, 700), "chain"),
+    (5, (3, 2), (3, 64), "none"),
+])
+def test_small_latents(n_h, sizes, lens, masks, dtype, d_c, d_R, splits):
+    inp = draw(sizes, lens, n_h, seed=n_h + d_c, masks=masks, width=(d_c, d_R), dtype=dtype)
+    for u_dtype in {dtype, torch.float32}:
+        u, lse = run(inp, splits, u_dtype)
+        mla.mla_check_device_errors()
+        check(inp, u, lse)
+        behind_is_untouched(inp, u, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_small_latents_other_branches_may_hold_anything(dtype, value):
+    inp = draw((4, 70 - 64), (130, 66), 16, seed=3, masks="chain", width=(64, 16), dtype=dtype)
+    mask = inp["mask"].cpu().numpy().view(np.uint64)
+    for b, n in enumerate((4, 6)):
+        c0 = int(inp["cu"][b])
+        mask[c0 + 2:c0 + n] &= np.uint64(~2 & (2 ** 64 - 1))  # token 1 is a leaf
+        row = rows_of(inp, b, int(inp["lens"][b]))[int(inp["lens"][b]) - n + 1]
+        inp["cache"][row, [5, 63, 70]] = value
+    inp["mask"] = torch.from_numpy(mask.view(np.int64)).cuda()
+    u, lse = run(inp, u_dtype=dtype)
+    mla.mla_check_device_errors()
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    for t, (ur, lr, du, dl) in reference(inp).items():
+        if t in (1, 5):
+            # the token itself: NaN, but where every product is -inf, whose
+            # weight is 0 (heads with q < 0 at all three places)
+            zero = (inp["q"][t][:, [5, 63, 70]] < 0).all(-1) & (value == float("inf"))
+            assert torch.equal(torch.isfinite(u[t].float()).all(-1), zero)
+            continue
+        assert ((u[t].double() - ur).abs() <= du + half * (ur.abs() + du)).all()
+        assert ((lse[t].double() - lr).abs() <= dl).all()
+
+
+def test_unsupported_widths_are_refused():
+    for width, dtype in (((512, 32), torch.bfloat16), ((512, 64), torch.float32), ((128, 8), torch.float32), ((72, 8), torch.bfloat16)):
+        inp = draw((2,), (70,), 4, width=width, dtype=dtype)
+        with pytest.raises(mla.MLAError) as e:
+            run(inp, u_dtype=dtype)
+        assert e.value.status == 2
