@@ -180,6 +180,7 @@ mla_status mla_decode_tree(const mla_tree_params* p, void* workspace, size_t wor
   a.u = p->u;
   a.lse = p->lse;
   a.rec = reinterpret_cast<int*>(w + L.rec);
+  a.seqs = reinterpret_cast<int4*>(w + L.seqs);
   a.up = reinterpret_cast<long long*>(w + L.up);
   a.cp = reinterpret_cast<int*>(w + L.cp);
   a.part_lse = reinterpret_cast<float*>(w + L.part_lse);
@@ -214,7 +215,7 @@ mla_status mla_build_tables(const mla_tables_params* p, void* stream) {
   if (p->B < 0 || p->max_tokens < 0 || p->n_free < 0 || p->page_size < 1 ||
       p->max_pages_per_seq < 1 || p->num_pages < 1)
     return MLA_ERR_INVALID_ARG;
-  if (p->B > kTablesMaxRequests || (long long)p->num_pages * p->page_size > INT_MAX ||
+  if (p->B > kTablesMaxRequests || p->max_tokens > INT_MAX - 1024 || (long long)p->num_pages * p->page_size > INT_MAX ||
       (long long)p->max_pages_per_seq * p->page_size > INT_MAX)
     return MLA_ERR_UNSUPPORTED;
   if (!p->free_used || !p->free_used_out || !p->cu_new || (p->n_free > 0 && !p->free_pages))

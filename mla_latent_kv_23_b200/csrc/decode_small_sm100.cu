@@ -106,12 +106,11 @@ struct Params {
   float scale_log2;    // softmax_scale * log2(e)
   // GQA path: groups, heads per group, key / value / RoPE blocks
   int n_g, hpg, d_h, d_v, nbk, nbr, nbv;
-  // trees: chunk records, prefix sums, mask words, packed tokens (q_map: the
-  // flat rows [T n_h, W], box (one 128-byte block) x 128)
+  // trees: chunk records, list of sequences, mask words (q_map: the flat rows
+  // [T n_h, W], box (one 128-byte block) x 128)
   const int* rec;
-  const int* cu_q;
+  const int4* seqs;
   const unsigned long long* mask;
-  int T;
 };
 
 template <bool kTf32, bool kGqa>
@@ -158,9 +157,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
   using Seg = std::conditional_t<kTree, TreeSegment, Segment>;
   auto start = [&](Walk& walk) {
     if constexpr (kTree)
-      walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, (long long)p.max_pages * p.page_size, chunk);
+      walk.init(p.rec, p.seqs, p.n_h, chunk);
     else
       walk.init(p.tile_prefix, p.chunk_t, p.chunk_b, p.header, p.B, chunk);
+  };
+  auto place = [](const Seg& sg) {  // of the segment's sequence in the batch
+    if constexpr (kTree) return sg.seq.b; else return sg.b;
   };
   auto length = [&](const Seg& sg) {
     if constexpr (kTree) return sg.seq.L; else return p.seqlens[sg.b];
@@ -231,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
                         sg.first);
           else if (kGqa)  // rows (r, h): query row r, head h of the group
             tma_load_3d(sbase + Lay::kOffQ + k * kQBlkBytes, &p.q_map, bar(Q_FULL), k * Lay::kCols,
-                        grp * p.hpg, sg.b * p.s_q);
+                        grp * p.hpg, place(sg) * p.s_q);
           else
             tma_load_3d(sbase + Lay::kOffQ + k * kQBlkBytes, &p.q_map, bar(Q_FULL), k * Lay::kCols,
-                        0, sg.b * p.s_q + qrow);
+                        0, place(sg) * p.s_q + qrow);
         }
-        const int* bt = p.block_table + (size_t)sg.b * p.max_pages;
+        const int* bt = p.block_table + (size_t)place(sg) * p.max_pages;
         for (int t = sg.t0; ok && t < sg.t1; ++t, ++g) {
           const int s = g % kStages, n = g / kStages;
           if (!(ok = mbar_wait(bar(KV_EMPTY + s), (n & 1) ^ 1, p.err, MLA_DEVFLAG_TIMEOUT))) break;
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_small_sm100_kernel(const _
         const int tok0 = (sg.t0 + j) * kTileTokens;
         unsigned long long clear = 0;  // tokens whose non-finite values must not meet P . C
         if constexpr (kTree) {
-          if (tok0 + kTileTokens > P0) {
+          if (tok0 > P0 - kTileTokens) {
             // bit k = position tok0 + k: the context, then the drafted tokens
             const int sh = tok0 - P0;  // > -64; at most n - 1
             const unsigned long long vis = sh >= 0 ? seen >> sh : (seen << -sh) | ((1ull << -sh) - 1);
@@ -748,9 +750,8 @@ cudaError_t launch_tree_small_sm100(const TreeArgs& a, const CUtensorMap& q_map,
   p.block_table = a.block_table;
   p.seqlens = a.seqlens;
   p.rec = a.rec;
-  p.cu_q = a.cu_q;
+  p.seqs = a.seqs;
   p.mask = a.mask;
-  p.T = a.T;
   p.u = a.u;
   p.lse = a.lse;
   p.part_u = a.part_u;

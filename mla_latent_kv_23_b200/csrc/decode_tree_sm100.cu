@@ -135,15 +135,14 @@ struct Params {
   const __nv_bfloat16* q;   // for L2 prefetch of the next segment's rows
   const __nv_bfloat16* kv;  // for L2 prefetch of tiles ahead of their loads
   const int* block_table;
-  const int* seqlens;
-  const int* cu_q;
   const unsigned long long* mask;
   const int* rec;
+  const int4* seqs;
   float* part_lse;
   void* u;
   float* lse;
   int* err;
-  int B, T, n_h, max_pages, page_size, num_pages;
+  int n_h, max_pages, page_size, num_pages;
   int out_f32;       // u is fp32 (else bf16)
   float scale_log2;  // softmax_scale * log2(e)
 };
@@ -233,7 +232,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = blockIdx.x >> 1;
-  const long long max_len = (long long)p.max_pages * p.page_size;
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
   // Signal a paired barrier of the even CTA: from the even CTA a local
   // arrival (with `announce`, the one arrival per phase that also expects the
@@ -301,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // tiles, from L2 if they are still there
     const uint64_t pol_once = l2_policy_evict_first(), pol_shared = l2_policy_evict_normal();
     TreeWalk walk;
-    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    walk.init(p.rec, p.seqs, p.n_h, chunk);
     TreeSegment sg;
     int g = 0;
     // A segment that ends before tile e stages its output in the stages of
@@ -312,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t tail_used = 0, tail_phase = 0;  // stages that held a tail tile; parity of its LOCAL_FULL's next phase
     bool ok = true;
     while (ok && walk.next(sg)) {
-      const int* bt = p.block_table + (size_t)sg.b * p.max_pages;
+      const int* bt = p.block_table + (size_t)sg.seq.b * p.max_pages;
       const int L = sg.seq.L;
       const uint64_t pol_stream = sg.seq.blocks == 1 ? pol_once : pol_shared;
       for (int t0 = sg.t0; ok && t0 < sg.t1; t0 += 32) {
@@ -396,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpRelay) {
     // ------------------------------------------------------------ relay
     TreeWalk walk;
-    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    walk.init(p.rec, p.seqs, p.n_h, chunk);
     TreeSegment sg;
     int g = 0, seg_i = 0;
     uint32_t tail_phase = 0;  // parity of each stage's next LOCAL_FULL phase
@@ -487,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdS = idesc_bf16(256, 128, false);
       constexpr uint32_t kIdPV = idesc_bf16(128, 256, true);
       TreeWalk walk;
-      walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+      walk.init(p.rec, p.seqs, p.n_h, chunk);
       TreeSegment sg;
       int g0 = 0, seg_i = 0;
       bool ok = true;
@@ -612,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
 
     TreeWalk walk;
-    walk.init(p.rec, p.cu_q, p.seqlens, p.B, p.T, p.n_h, max_len, chunk);
+    walk.init(p.rec, p.seqs, p.n_h, chunk);
     TreeSegment sg;
     int g = 0;
     bool ok = true;
@@ -629,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a tile that reaches into the drafted tokens: which of them this
         // thread's rows see (none for rows past the block's last, whose
         // results are not written), read while S of the tile runs
-        const bool tail = tok0 + kTreeTile > P0;
+        const bool tail = tok0 > P0 - kTreeTile;
         unsigned long long seen[2] = {0, 0};
         if (tail) {
 #pragma unroll
@@ -1004,16 +1002,13 @@ cudaError_t launch_tree_sm100(const TreeArgs& a, const TreeMaps& maps, cudaStrea
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.kv = static_cast<const __nv_bfloat16*>(a.kv);
   p.block_table = a.block_table;
-  p.seqlens = a.seqlens;
-  p.cu_q = a.cu_q;
   p.mask = a.mask;
   p.rec = a.rec;
+  p.seqs = a.seqs;
   p.part_lse = a.part_lse;
   p.u = a.u;
   p.lse = a.lse;
   p.err = a.err;
-  p.B = a.B;
-  p.T = a.T;
   p.n_h = a.n_h;
   p.max_pages = a.max_pages;
   p.page_size = a.page_size;

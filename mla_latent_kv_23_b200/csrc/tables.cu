@@ -10,6 +10,7 @@
 #include "mla.h"
 #include "tables.h"
 #include "tree.h"
+#include "tree_schedule.cuh"
 
 namespace mla {
 namespace {
@@ -310,15 +311,11 @@ constexpr int kAccSlices = 9;  // 1152 bytes a pass: a bf16 row of 576 values
 __global__ void __launch_bounds__(kAccThreads) accept_tree_kernel(const __grid_constant__ AcceptArgs a) {
   const int b = blockIdx.x;
   const int i = threadIdx.x >> 3, k = threadIdx.x & 7;
-  const int row0 = a.cu_q[b], end = a.cu_q[b + 1], L = a.seqlens[b], node = a.accepted[b];
-  int flags = 0;
-  int n = 0;
-  if (row0 < 0 || end < row0 || end > a.T || end - row0 > kTreeMaxNodes)
-    flags |= MLA_DEVFLAG_BAD_TREE;
-  else
-    n = end - row0;
-  const bool good = L >= n && L <= (long long)a.max_pages * a.page_size;
-  if (!good) flags |= MLA_DEVFLAG_BAD_SEQLEN;
+  const TreeSeq seq = tree_seq(a.cu_q, a.seqlens, b, a.T, 1, (long long)a.max_pages * a.page_size);
+  const int node = a.accepted[b];
+  const int row0 = seq.row0, n = seq.n, L = seq.L;
+  int flags = seq.flag;
+  const bool good = flags != MLA_DEVFLAG_BAD_SEQLEN;
   if (node < -1 || node >= n) flags |= MLA_DEVFLAG_BAD_TREE;
   unsigned long long mask = 0;
   if (good && node >= 0 && node < n) mask = (unsigned long long)a.tree_mask[row0 + node];

@@ -17,16 +17,17 @@ constexpr int kTreeRows = 128;     // (token, head) rows of one row block
 // output of the last), in 64-token tiles.
 constexpr int kTreeSegTiles = 4;
 
-// Workspace of mla_decode_tree.  rec: 8 ints per chunk boundary (G + 1 of
-// them): sequence, row block and tile where the chunk starts, 0, then that
-// sequence's first token, drafted tokens and length, 0; the last one is
-// (B, 0, ...).  up / cp: per-sequence prefix sums of the plan, used there
+// Workspace of mla_decode_tree.  seqs: the sequences with work, in order, 4 ints
+// each (first token, drafted tokens, length, place in the batch).  rec: 8 ints
+// per chunk boundary (G + 1 of them): place on that list, row block and tile
+// where the chunk starts, 0, then the list's entry; the last one is (list's
+// length, 0, ...).  up / cp: prefix sums of the plan over the list, used there
 // only when the batch is too large for shared memory.  part_u / part_lse: the
 // partial results of pieces of row blocks, 128 rows per slot: chunk c writes a
 // piece that continues a block into slot 2c and one that begins a block in
 // slot 2c + 1 (fp32).
 struct TreeWsLayout {
-  size_t rec = 0, up = 0, cp = 0, part_lse = 0, part_u = 0, total = 0;
+  size_t rec = 0, seqs = 0, up = 0, cp = 0, part_lse = 0, part_u = 0, total = 0;
 };
 TreeWsLayout tree_ws_layout(int B, int d_c, int num_chunks);
 
@@ -40,6 +41,7 @@ struct TreeArgs {
   void* u;
   float* lse;
   int* rec;
+  int4* seqs;
   long long* up;
   int* cp;
   float* part_u;

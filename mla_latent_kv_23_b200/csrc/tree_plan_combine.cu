@@ -62,8 +62,8 @@ __device__ long long block_scan(long long v, long long* warp_sums, long long* to
 
 __global__ void __launch_bounds__(kPlanThreads)
     tree_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ seqlens, int B, int T,
-                     int n_h, long long max_len, int num_chunks, int* rec, long long* up_ws,
-                     int* cp_ws, int* err) {
+                     int n_h, long long max_len, int num_chunks, int* rec, int4* seqs,
+                     long long* up_ws, int* cp_ws, int* err) {
   ptx::pdl_launch_dependents();
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ long long up_s[kPlanSmemSeqs + 1];
@@ -71,89 +71,95 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int longest_piece;
   constexpr int K = kTreeSegTiles;
   const bool on_chip = B <= kPlanSmemSeqs;
-  long long* up = on_chip ? up_s : up_ws;  // units before sequence b on the line
-  int* cp = on_chip ? cp_s : cp_ws;        // chunks before sequence b when cut into pieces
+  long long* up = on_chip ? up_s : up_ws;  // units before place k of the list on the line
+  int* cp = on_chip ? cp_s : cp_ws;        // chunks before place k when cut into pieces
   long long units_all = 0, blocks_all = 0, total;
+  int listed = 0;
   int flags = 0;
   if (threadIdx.x == 0) longest_piece = 0;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    long long units = 0, blocks = 0;
-    if (i < B) {
-      const TreeSeq s = tree_seq(cu_q, seqlens, i, T, n_h, max_len);
-      flags |= s.flag;
-      blocks = s.blocks;
-      units = blocks * (s.tiles + K);
-    }
+    TreeSeq s = {};
+    if (i < B) s = tree_seq(cu_q, seqlens, i, T, n_h, max_len);
+    flags |= s.flag;
+    const long long units = (long long)s.blocks * (s.tiles + K);
     const long long incl = block_scan(units, warp_sums, &total);
-    if (i < B) up[i] = units_all + incl - units;
+    const int work = s.blocks > 0;
+    // row blocks (high half) and sequences with work (low half)
+    long long both;
+    const long long at = block_scan(((long long)s.blocks << 32) | work, warp_sums, &both);
+    if (work) {
+      const int k = listed + (int)(at & 0xffffffff) - 1;
+      seqs[k] = make_int4(s.row0, s.n, s.L, i);
+      up[k] = units_all + incl - units;
+    }
     units_all += total;
-    block_scan(blocks, warp_sums, &total);
-    blocks_all += total;
+    blocks_all += both >> 32;
+    listed += (int)(both & 0xffffffff);
   }
   if (flags) atomicOr(err, flags);
-  if (threadIdx.x == 0) up[B] = units_all;
+  if (threadIdx.x == 0) up[listed] = units_all;
+  __syncthreads();
   const long long tiles_all = units_all - K * blocks_all;
   const long long per = units_all > 0 ? (units_all + num_chunks - 1) / num_chunks : 1;
   const bool fits = blocks_all > 0 && blocks_all <= num_chunks;
-  // pieces of each of sequence i's blocks
+  // pieces of each of a sequence's blocks
   auto pieces = [&](const TreeSeq& s) -> int {
-    if (s.blocks == 0) return 0;
     if (s.tiles <= kWholeTiles) return 1;
     const long long n = 1 + (num_chunks - blocks_all) * s.tiles / tiles_all;
     return (int)min(n, (long long)(s.tiles + 1) / 2);
   };
   if (fits) {
     long long chunks = 0;
-    for (int base = 0; base < B; base += kPlanThreads) {
-      const int i = base + threadIdx.x;
+    for (int base = 0; base < listed; base += kPlanThreads) {
+      const int k = base + threadIdx.x;
       int n = 0;
-      if (i < B) {
-        const TreeSeq s = tree_seq(cu_q, seqlens, i, T, n_h, max_len);
+      if (k < listed) {
+        const TreeSeq s = tree_listed(seqs[k], n_h);
         const int p = pieces(s);
         n = p * s.blocks;
-        if (p > 0) atomicMax(&longest_piece, (s.tiles + p - 1) / p);
+        atomicMax(&longest_piece, (s.tiles + p - 1) / p);
       }
       const long long incl = block_scan(n, warp_sums, &total);
-      if (i < B) cp[i] = (int)(chunks + incl - n);
+      if (k < listed) cp[k] = (int)(chunks + incl - n);
       chunks += total;
     }
-    if (threadIdx.x == 0) cp[B] = (int)chunks;
+    if (threadIdx.x == 0) cp[listed] = (int)chunks;
   }
   __syncthreads();
   const bool cut_pieces = fits && longest_piece <= per + K;
   for (int c = threadIdx.x; c <= num_chunks; c += kPlanThreads) {
-    int b = B, g = 0, t = 0;
-    TreeSeq first = {0, 0, 0, 0, 0, 0};
-    if (cut_pieces ? c < cp[B] : c * per < units_all) {
+    int k = listed, g = 0, t = 0;
+    int4 first = make_int4(0, 0, 0, 0);
+    if (cut_pieces ? c < cp[listed] : c * per < units_all) {
       const long long x = cut_pieces ? c : c * per;
-      int lo = 0, hi = B;  // the largest b that starts at or before x
+      int lo = 0, hi = listed;  // the largest k that starts at or before x
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if ((cut_pieces ? (long long)cp[mid] : up[mid]) <= x) lo = mid; else hi = mid;
       }
-      b = lo;
-      const TreeSeq s = tree_seq(cu_q, seqlens, b, T, n_h, max_len);
+      k = lo;
+      first = seqs[k];
+      const TreeSeq s = tree_listed(first, n_h);
       if (cut_pieces) {
-        const int p = pieces(s), k = c - cp[b];
-        g = k / p;
-        t = (int)((long long)(k % p) * s.tiles / p);
+        const int p = pieces(s), i = c - cp[k];
+        g = i / p;
+        t = (int)((long long)(i % p) * s.tiles / p);
       } else {
-        const long long off = x - up[b];
+        const long long off = x - up[k];
         g = (int)(off / (s.tiles + K));
         t = (int)(off % (s.tiles + K)) - K;
         if (t <= kSnap) {
           t = 0;
         } else if (s.tiles - t <= kSnap) {
           t = 0;
-          ++g;  // past the sequence's last block: the walk goes on to the next sequence
+          ++g;  // past the sequence's last block: the walk goes on to the next one
         }
       }
-      first = s;
     }
     int4* r = reinterpret_cast<int4*>(rec) + 2 * c;
-    r[0] = make_int4(b, g, t, 0);
-    r[1] = make_int4(first.row0, first.n, first.L, 0);
+    r[0] = make_int4(k, g, t, 0);
+    r[1] = first;
   }
 }
 
@@ -296,6 +302,8 @@ TreeWsLayout tree_ws_layout(int B, int d_c, int num_chunks) {
   size_t off = 0;
   L.rec = off;
   off = up256(off + sizeof(int) * 8 * ((size_t)num_chunks + 1));
+  L.seqs = off;
+  off = up256(off + sizeof(int) * 4 * (size_t)B);
   L.up = off;
   off = up256(off + sizeof(long long) * ((size_t)B + 1));
   L.cp = off;
@@ -311,7 +319,7 @@ TreeWsLayout tree_ws_layout(int B, int d_c, int num_chunks) {
 cudaError_t launch_tree_plan(const TreeArgs& a, cudaStream_t s) {
   tree_plan_kernel<<<1, kPlanThreads, 0, s>>>(a.cu_q, a.seqlens, a.B, a.T, a.n_h,
                                               (long long)a.max_pages * a.page_size, a.num_chunks,
-                                              a.rec, a.up, a.cp, a.err);
+                                              a.rec, a.seqs, a.up, a.cp, a.err);
   return cudaGetLastError();
 }
 

@@ -5,8 +5,8 @@
 // They are taken in blocks of 128 rows, the M dimension of the contractions:
 // one block per token at 128 heads, eight tokens per block at 16 heads.  A
 // block crosses every 64-token tile of its sequence; a chunk is a run of
-// (sequence, block, tile) in that order, given by where it and the next chunk
-// start, and the part of a chunk inside one block is a segment.  A segment
+// (sequence, block, tile) in that order, over the sequences that have work,
+// given by where it and the next chunk start, and the part of a chunk inside one block is a segment.  A segment
 // that covers a whole block writes u and lse, any other a partial result.
 #pragma once
 
@@ -19,6 +19,7 @@ namespace mla {
 // where what the host cannot see is wrong (flag != 0): nothing is read or
 // written out of range for it.
 struct TreeSeq {
+  int b;       // its place in the batch
   int row0;    // its first token of the packed rows
   int n;       // drafted tokens, the last n of its L cached ones
   int L;
@@ -36,6 +37,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const int* __restrict__ cu_q,
                                             const int* __restrict__ seqlens, int b, int T, int n_h,
                                             long long max_len) {
   TreeSeq s;
+  s.b = b;
   s.row0 = cu_q[b];
   const int end = cu_q[b + 1];
   s.L = seqlens[b];
@@ -58,7 +60,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const int* __restrict__ cu_q,
 }
 
 struct TreeSegment {
-  int b, g;    // sequence, row block
+  int g;       // row block
   int t0, t1;  // tiles
   int whole;   // covers every tile of the block
   int slot;    // partial slot where it does not
@@ -67,57 +69,52 @@ struct TreeSegment {
   TreeSeq seq;
 };
 
-struct TreeWalk {
-  const int *cu_q, *seqlens;
-  int B, T, n_h, chunk;
-  long long max_len;
-  int b, g, t;     // next tile
-  int be, ge, te;  // where the next chunk starts
-  bool loaded;
-  TreeSeq seq;
+// The plan's list of the sequences that have work: token, count, length, place.
+__device__ __forceinline__ TreeSeq tree_listed(int4 v, int n_h) {
+  TreeSeq s;
+  s.row0 = v.x;
+  s.n = v.y;
+  s.L = v.z;
+  s.b = v.w;
+  s.flag = 0;
+  tree_extent(s, n_h);
+  return s;
+}
 
-  __device__ __forceinline__ void init(const int* rec, const int* cu, const int* lens, int nseq,
-                                       int rows, int heads, long long longest, int chunk_id) {
-    cu_q = cu;
-    seqlens = lens;
-    B = nseq;
-    T = rows;
+struct TreeWalk {
+  const int4* seqs;
+  int n_h, chunk;
+  int k, g, t;     // next tile: place on the list, row block, tile
+  int ke, ge, te;  // where the next chunk starts
+  TreeSeq seq;     // of place k
+
+  __device__ __forceinline__ void init(const int* rec, const int4* list, int heads, int chunk_id) {
+    seqs = list;
     n_h = heads;
-    max_len = longest;
     chunk = chunk_id;
     const int4* r = reinterpret_cast<const int4*>(rec) + 2 * chunk_id;
     const int4 r0 = r[0], s0 = r[1], r1 = r[2];  // independent: one memory round trip
-    b = r0.x;
+    k = r0.x;
     g = r0.y;
     t = r0.z;
-    be = r1.x;
+    ke = r1.x;
     ge = r1.y;
     te = r1.z;
-    // the first sequence comes with the record
-    seq.row0 = s0.x;
-    seq.n = s0.y;
-    seq.L = s0.z;
-    seq.flag = 0;
-    tree_extent(seq, n_h);
-    loaded = true;
+    seq = tree_listed(s0, n_h);
   }
 
   __device__ __forceinline__ bool next(TreeSegment& s) {
     while (true) {
-      if (b >= B || b > be || (b == be && (g > ge || (g == ge && t >= te)))) return false;
-      if (!loaded) {
-        seq = tree_seq(cu_q, seqlens, b, T, n_h, max_len);
-        loaded = true;
-      }
+      if (k > ke || (k == ke && (g > ge || (g == ge && t >= te)))) return false;
       if (g < seq.blocks) break;
-      ++b;
+      ++k;
       g = t = 0;
-      loaded = false;
+      // (the chunks end at the list's end, which has no entry)
+      if (k < ke || te > 0 || ge > 0) seq = tree_listed(seqs[k], n_h);
     }
-    s.b = b;
     s.g = g;
     s.t0 = t;
-    s.t1 = (b == be && g == ge) ? min(te, seq.tiles) : seq.tiles;
+    s.t1 = (k == ke && g == ge) ? min(te, seq.tiles) : seq.tiles;
     s.whole = t == 0 && s.t1 == seq.tiles;
     s.slot = 2 * chunk + (t == 0 ? 1 : 0);
     s.first = seq.row0 * n_h + g * kTreeRows;

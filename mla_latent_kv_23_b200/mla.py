@@ -509,7 +509,7 @@ def tree_params(q, kv_cache, block_table, seqlens, cu_q, tree_mask, u, lse, page
     d_c = W - d_R
     if kv_cache.dtype != q.dtype or (u.dtype != q.dtype and u.dtype != torch.float32):
         raise TypeError("kv_cache must have the dtype of q, u that or float32")
-    if kv_cache.dim() != 2 or kv_cache.shape[1] != W or kv_cache.shape[0] % page_size != 0:
+    if page_size < 1 or kv_cache.dim() != 2 or kv_cache.shape[1] != W or kv_cache.shape[0] % page_size != 0:
         raise ValueError("kv_cache must be [num_pages * page_size, d_c + d_R]")
     if tuple(u.shape) != (T, n_h, d_c):
         raise ValueError("u must be [T, n_h, d_c]")
@@ -540,6 +540,8 @@ def mla_decode_tree_workspace_size(p: TreeParams) -> int:
 
 def mla_decode_tree(p: TreeParams, workspace, stream=None) -> None:
     """Attention of drafted trees over the paged latent cache."""
+    if workspace.get_device() != p.device:
+        raise ValueError("the workspace must be on the tensors' device")
     with _On(p.device):
         _check(lib().mla_decode_tree(p.ref, _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -553,7 +555,7 @@ def accept_params(kv_cache, block_table, seqlens, cu_q, tree_mask, accepted, seq
     seqlens), cu_q [B + 1], tree_mask (int64) and path [T]."""
     torch = _torch()
     B, T = seqlens.shape[0], path.shape[0]
-    if kv_cache.dim() != 2 or kv_cache.shape[0] % page_size != 0:
+    if page_size < 1 or kv_cache.dim() != 2 or kv_cache.shape[0] % page_size != 0:
         raise ValueError("kv_cache must be [num_pages * page_size, d_c + d_R]")
     _int_tensor(block_table, "block_table", (B, None))
     for t, name, size in ((seqlens, "seqlens", B), (cu_q, "cu_q", B + 1), (accepted, "accepted", B),

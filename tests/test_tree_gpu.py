@@ -177,6 +177,28 @@ def test_many_blocks_over_chunks(n_h, splits):
         behind_is_untouched(inp, u, lse)
 
 
+@pytest.mark.parametrize("B,splits", [(700, 0), (3000, 0), (3000, 2)])
+def test_many_idle_sequences(B, splits):
+    # few of many sequences have drafted tokens; batches on both sides of what
+    # the plan keeps on chip
+    rng = np.random.default_rng(B)
+    sizes = np.zeros(B, int)
+    sizes[rng.choice(B, 9, replace=False)] = rng.integers(1, 20, 9)
+    sizes[0], sizes[-1] = 3, 5
+    inp = draw(tuple(sizes.tolist()), tuple((sizes + rng.integers(0, 200, B)).tolist()), 16, seed=B)
+    u, lse = run(inp, splits)
+    mla.mla_check_device_errors()
+    check(inp, u, lse)
+    behind_is_untouched(inp, u, lse)
+
+
+def test_nothing_drafted():
+    inp = draw((0, 0), (70, 5), 16)
+    u, lse = run(inp)
+    mla.mla_check_device_errors()
+    assert (u == -7).all() and (lse == -7).all()
+
+
 def test_without_lse():
     inp = draw((3, 4), (100, 200), 32, seed=3)
     u, _ = run(inp, with_lse=False)
