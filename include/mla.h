@@ -420,7 +420,9 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  * the token's depth, which is its RoPE position, and bit k of tree_mask[t] is
  * set for k = i and the tokens on its branch before it.  Tokens of a request
  * of more than 64 are a prompt: their parents are not read, tree_mask[t] = 0.
- * Entries of seq_ids, pos, slots and tree_mask past the total are not written.
+ * Entries of seq_ids, pos, slots and tree_mask past the total are not written
+ * (a captured step whose number of tokens varies sets slots to -1 before the
+ * call: mla_append_latent_slots skips such tokens).
  *
  * Device flags: MLA_DEVFLAG_BAD_SEQLEN (a negative length, one past the block
  * table, pages_held below have_b or above the block table: the request gets no

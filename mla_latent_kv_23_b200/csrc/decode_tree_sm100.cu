@@ -531,11 +531,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         umma_commit_pair(bar(KV_EMPTY + g % kStages), kBothCtas);
         umma_commit_pair(bar(PV_DONE + (g & 1)), kBothCtas);
       };
-      // Fixed order per segment: S0 S1 S2, then P.C(j) S(j+3) for every tile
-      // j, so S runs two tiles ahead of P.C and the softmax of tile j has
-      // two S groups of tensor work to hide behind.  Each step polls only the
-      // barriers it needs (a barrier test costs ~150 cycles; re-testing a
-      // ready barrier is not free).
+      // S runs up to two tiles ahead of P . C (its two buffers), so the softmax
+      // of a tile has two S of tensor work to hide behind.
       auto wait = [&](int b, uint32_t parity) {
         return mbar_wait(bar(b), parity, p.err, MLA_DEVFLAG_TIMEOUT);
       };
