@@ -405,6 +405,19 @@ def _one_device(*tensors) -> int:
     return dev
 
 
+def _pointers(*tensors):
+    """(device index, pointers) of tensors on one CUDA device, in one pass."""
+    dev = tensors[0].get_device()
+    at = []
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        at.append(t.data_ptr())
+    return dev, at
+
+
 class _On:
     """Makes a device current for a call: the library works on the current
     one.  A stream handle stays the caller's."""
@@ -451,11 +464,10 @@ def mla_append_latent_slots(h, W_DKV, W_KR, slots, pos, kv_cache, rope_base: flo
         raise ValueError("slots and pos must have one entry per token")
     if T == 0:
         return
-    with _On(_one_device(h, W_DKV, W_KR, slots, pos, kv_cache)):
-        _check(lib().mla_append_latent_slots(_ptr(h), _ptr(W_DKV), _ptr(W_KR), _ptr(slots), _ptr(pos),
-                                             _ptr(kv_cache), rows, T, d_model, d_c, d_R,
-                                             float(rope_base), _dtype_code(h), _stream(stream)),
-               "mla_append_latent_slots")
+    dev, at = _pointers(h, W_DKV, W_KR, slots, pos, kv_cache)
+    with _On(dev):
+        _check(lib().mla_append_latent_slots(*at, rows, T, d_model, d_c, d_R, rope_base, _dtype_code(h),
+                                             _stream(stream)), "mla_append_latent_slots")
 
 
 def tables_params(ctx_lens, new_lens, block_table, free_pages, free_used, free_used_out, seqlens,

@@ -153,6 +153,13 @@ def test_tables_of_many(B, most):
     Tables(ctx, new, parents=random_parents(new, rng)).check()
 
 
+def test_a_wide_block_table():
+    # so many columns that sums over the requests might pass 32 bits
+    rng = np.random.default_rng(5)
+    ctx, new = rng.integers(0, 500, 600).tolist(), rng.integers(0, 200, 600).tolist()
+    Tables(ctx, new, max_pages=60000, parents=random_parents(new, rng)).check()
+
+
 def test_chains_and_stars_of_64():
     for up in (list(range(-1, 63)), [-1] * 64, [-1] + [0] * 63, [-1, 0] + [i // 2 for i in range(2, 64)]):
         Tables((77,), (64,), parents=up).check()
