@@ -120,6 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1) append_slots_kernel(const __grid_
   // what the epilogue needs of this thread's token, read ahead
   const int my_slot = (int)threadIdx.x < nt ? p.slots[t0 + threadIdx.x] : -1;
   const int my_pos = (int)threadIdx.x < nt && p.d_R > 0 ? p.pos[t0 + threadIdx.x] : 0;
+  if (threadIdx.x == 64) {
+    prefetch_tmap(&p.x_map);
+    prefetch_tmap(&p.w_map[box0 < nd ? 0 : 1]);
+  }
   const int copies = 1 + boxes;  // a block: the tokens, then the weight boxes
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
