@@ -63,11 +63,11 @@ TreeKernel tree_kernel(const mla_tree_params* p, const DeviceInfo* d) {
 }
 
 // One chunk per resident cluster, but no more than the batch can have tiles by
-// what the host knows (row blocks times the block table's width): starting and
+// what the host knows (the most row blocks times the block table's width): starting and
 // retiring 148 CTAs of 226 KB takes longer than the work of a small call.
 int tree_chunks(const mla_tree_params* p, const DeviceInfo* d) {
   if (p->num_splits > 0) return p->num_splits;
-  const long long blocks = p->B + (long long)p->T * p->n_h / kTreeRows;
+  const long long blocks = ((long long)p->T * p->n_h + (kTreeRows - 1LL) * p->B) / kTreeRows;
   const long long tiles = (long long)p->max_pages_per_seq * p->page_size / kTreeTile;
   const long long most = blocks * tiles;
   const int resident = tree_kernel(p, d) == TreeKernel::kV3 ? d->tree_clusters : d->sm_count;
