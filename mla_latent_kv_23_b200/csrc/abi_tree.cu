@@ -100,31 +100,21 @@ mla_status encode_tree(TreeMaps* m, const mla_tree_params* p, const TreeArgs& a)
   constexpr cuuint64_t kRow = 576 * 2;  // bytes of a cache or query row
   constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
-  constexpr auto k64 = CU_TENSOR_MAP_SWIZZLE_64B;
   bool ok = true;
+  {  // (column, row, 64-column block)
+    const cuuint64_t dims[3] = {64, kvrows, 9}, strides[2] = {kRow, 128};
+    const cuuint32_t box[3] = {64, 32, 9};
+    ok &= encode(&m->k, kBf16, 3, p->kv_cache, dims, strides, box, k128);
+  }
   {  // (column, row, block & 1, block >> 1): a CTA's columns 128 r + {0, 64, 256, 320} in one copy
     const cuuint64_t dims[4] = {192, kvrows, 2, 2}, strides[3] = {kRow, 128, 512};
     const cuuint32_t box[4] = {64, 64, 2, 2};
-    ok &= encode(&m->kv_lat4, kBf16, 4, p->kv_cache, dims, strides, box, k128);
+    ok &= encode(&m->v, kBf16, 4, p->kv_cache, dims, strides, box, k128);
   }
   {
-    const cuuint64_t dims[2] = {576, kvrows}, strides[1] = {kRow};
-    const cuuint32_t box[2] = {32, 64};
-    ok &= encode(&m->kv_rope, kBf16, 2, p->kv_cache, dims, strides, box, k64);
-  }
-  m->has_q4 = p->n_h % 16 == 0;
-  if (m->has_q4) {  // (column, row within 16, column half, 16 rows)
-    const cuuint64_t dims[4] = {384, 16, 2, rows / 16}, strides[3] = {kRow, 256, 16 * kRow};
-    const cuuint32_t box[4] = {64, 16, 2, 4};
-    ok &= encode(&m->q_lat4, kBf16, 4, p->q, dims, strides, box, k128);
-    const cuuint64_t rdims[4] = {544, 16, 2, rows / 16}, rstrides[3] = {kRow, 64, 16 * kRow};
-    const cuuint32_t rbox[4] = {32, 16, 2, 4};
-    ok &= encode(&m->q_rope4, kBf16, 4, p->q, rdims, rstrides, rbox, k64);
-  } else {
-    const cuuint64_t dims[2] = {576, rows}, strides[1] = {kRow};
-    const cuuint32_t box[2] = {64, 16}, rbox[2] = {32, 16};
-    ok &= encode(&m->q_lat, kBf16, 2, p->q, dims, strides, box, k128);
-    ok &= encode(&m->q_rope, kBf16, 2, p->q, dims, strides, rbox, k64);
+    const cuuint64_t dims[3] = {64, rows, 9}, strides[2] = {kRow, 128};
+    const cuuint32_t box[3] = {64, 64, 3};
+    ok &= encode(&m->q, kBf16, 3, p->q, dims, strides, box, k128);
   }
   {  // 128-byte lines of 32 rows
     const cuuint64_t dims[2] = {512, rows}, strides[1] = {512u * (a.out_f32 ? 4 : 2)};

@@ -58,15 +58,11 @@ cudaError_t launch_tree_combine(const TreeArgs& a, cudaStream_t s);
 
 // The DeepSeek-V3-shape attend kernel: bf16, d_c = 512, d_R = 64.  The rows of
 // q [T, n_h, 576] and u [T, n_h, 512] are flat: row t n_h + h.
-//   kv_lat4 / kv_rope: one CTA's latent blocks of 64 cache rows in one copy,
-//     and its RoPE block;
-//   q_lat4 / q_rope4 (n_h a multiple of 16, has_q4): a CTA's 64 rows, both
-//     column halves, in one copy per 64-column block;
-//   q_lat / q_rope: 16 rows of one column half;
+//   k: 32 cache rows, all nine 64-column blocks; v: one CTA's four latent blocks
+//     of 64 cache rows; q: 64 rows, three 64-column blocks (a copy each);
 //   u_out: 32 rows of u, 128 bytes of columns; part_out the same of part_u.
 struct TreeMaps {
-  CUtensorMap kv_lat4, kv_rope, q_lat4, q_rope4, q_lat, q_rope, u_out, part_out;
-  int has_q4;
+  CUtensorMap k, v, q, u_out, part_out;
 };
 int tree_sm100_prepare();  // co-resident clusters, 0 if the kernel cannot run
 cudaError_t launch_tree_sm100(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);
