@@ -318,18 +318,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else
             tma_load_3d_to_pair_hint(sbase + kOffQ + c * kQBlk, &p.maps.q, mapa(bar(Q_FULL), 0), 0, y, c, pol);
         }
-        // the next segment's rows go to L2 now
-        TreeWalk peek = walk;
-        TreeSegment nx;
-        if (peek.next(nx) && nx.rows > 64 * (int)rank) {
-          const __nv_bfloat16* src = p.q + ((size_t)nx.first + 64 * rank) * (kDc + 64);
-          const uint32_t bytes =
-              static_cast<uint32_t>(min(64, nx.rows - 64 * (int)rank)) * (kDc + 64) * 2;
-          for (uint32_t off = 0; off < bytes; off += 16384)
-            bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(src) + off, min(16384u, bytes - off));
-        }
       }
       __syncwarp();
+    };
+    // the next segment's rows go to L2
+    auto prefetch_next_q = [&]() {
+      TreeWalk peek = walk;
+      TreeSegment nx;
+      if (peek.next(nx) && nx.rows > 64 * (int)rank && elect_one()) {
+        const __nv_bfloat16* src = p.q + ((size_t)nx.first + 64 * rank) * (kDc + 64);
+        const uint32_t bytes = static_cast<uint32_t>(min(64, nx.rows - 64 * (int)rank)) * (kDc + 64) * 2;
+        for (uint32_t off = 0; off < bytes; off += 16384)
+          bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(src) + off, min(16384u, bytes - off));
+      }
+      __syncwarp();
+    };
+    // 64 rows of a page that a 64-token tile reads: contiguous bytes
+    auto prefetch_tile = [&](int page, int t) {
+      const int tok = t * kTreeTile;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(
+          p.kv + ((size_t)page * p.page_size + tok % p.page_size) * (kDc + 64));
+      constexpr uint32_t kTile = kTreeTile * (kDc + 64) * 2;
+      for (uint32_t off = 0; off < kTile; off += 16384) bulk_prefetch_l2(src + off, min(16384u, kTile - off));
     };
     while (ok && walk.next(sg)) {
       // (after the first segment a K slot is free before the query area)
@@ -339,21 +349,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n_here = min(32, sg.t1 - t0);
         for (int i = 0; ok && i < n_here; ++i, ++g) {
           const int page = __shfl_sync(0xffffffffu, my_page, i);
-          // The tile kPrefetchAhead tiles later goes to L2 now: its copy is
+          // The tile kPrefetchAhead tiles later goes to L2 now: its copies are
           // issued only when a slot frees, and an L2 hit then lands in a
-          // fraction of the HBM latency.  A 64-token tile of one page is 64 x
-          // 1152 contiguous bytes; the even CTA fetches all of it.  At the
+          // fraction of the HBM latency.  The even CTA fetches all of it.  At the
           // start of a chunk every SM is already loading its queries and first
-          // tiles: the first kPrefetchAhead of the chunk prefetch nothing.
+          // tiles: the first prefetch comes behind those, below.
           const int page_ahead = __shfl_sync(0xffffffffu, my_page, (i + kPrefetchAhead) & 31);
-          if (leader && g >= kPrefetchAhead && i + kPrefetchAhead < n_here && elect_one()) {
-            const int tok_a = (t0 + i + kPrefetchAhead) * kTreeTile;
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                p.kv + ((size_t)page_ahead * p.page_size + tok_a % p.page_size) * (kDc + 64));
-            constexpr uint32_t kTile = kTreeTile * (kDc + 64) * 2;
-            for (uint32_t off = 0; off < kTile; off += 16384)
-              bulk_prefetch_l2(src + off, min(16384u, kTile - off));
-          }
+          if (leader && g >= 2 && i + kPrefetchAhead < n_here && elect_one())
+            prefetch_tile(page_ahead, t0 + i + kPrefetchAhead);
           const int s = g & 1;
           if (!(ok = warp_wait(bar(K_EMPTY + s), ((g >> 1) & 1) ^ 1, p.err))) break;
           if (elect_one()) {
@@ -369,6 +372,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (seg_i > 0 && t0 + i == sg.t0) load_q(sg);
+          if (t0 + i == min(sg.t0 + 1, sg.t1 - 1)) {
+            if (seg_i == 0) {  // (i = 1 here if there are more tiles)
+              for (int k = 1; k <= kPrefetchAhead; ++k) {
+                const int pg = __shfl_sync(0xffffffffu, my_page, (i + k) & 31);
+                if (leader && i + k < n_here && elect_one()) prefetch_tile(pg, t0 + i + k);
+              }
+            }
+            prefetch_next_q();
+          }
         }
       }
       ++seg_i;
