@@ -236,6 +236,27 @@ def test_other_branches_may_hold_anything(value, n_h):
                 assert ((lse[c0 + r].double() - lr).abs() <= dl).all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n_h", [128, 12])
+@pytest.mark.parametrize("length", [64, 101, 159, 160])
+def test_tokens_nobody_sees_may_hold_anything(value, n_h, length):
+    # of 64 drafted tokens, in tiles of 64 positions, at both ends of each half
+    # of a tile and across two of them; whole rows of the value
+    inp = draw((64, 3), (length, 70), n_h, seed=length, masks="chain")
+    hidden = {0, 7, 26, 27, 31, 32, 58, 59, 63}
+    mask = inp["mask"].cpu().numpy().view(np.uint64)
+    for r in range(64):
+        mask[r] &= np.uint64((2 ** 64 - 1) & ~sum(1 << h for h in hidden))
+    inp["mask"] = torch.from_numpy(mask.view(np.int64)).cuda()
+    rows = rows_of(inp, 0, length)
+    for h in hidden:
+        inp["cache"][rows[length - 64 + h]] = value
+    u, lse = run(inp)
+    mla.mla_check_device_errors()
+    check(inp, u, lse)
+    behind_is_untouched(inp, u, lse)
+
+
 def test_large_scores_move_the_maximum():
     # scores that climb by 2^20 ... 2^50 from tile to tile, past every decision
     # to rescale
