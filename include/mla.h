@@ -425,8 +425,12 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  * call: mla_append_latent_slots skips such tokens).
  *
  * Device flags: MLA_DEVFLAG_BAD_SEQLEN (a negative length, one past the block
- * table, pages_held below have_b or above the block table: the request gets no
- * tokens and seqlens[b] = 0), MLA_DEVFLAG_NO_PAGES (the free list ran out, or
+ * table, pages_held below what ctx_b takes or above the block table: the request
+ * gets no tokens and no pages.  With pages_held it is otherwise as it was, so
+ * that the outputs can be carried on: pages_held_out[b] = pages_held[b] if the
+ * block table is that wide, else 0, and seqlens[b] = ctx_b if ctx_b and
+ * pages_held[b] are in order, else 0; without pages_held seqlens[b] = 0),
+ * MLA_DEVFLAG_NO_PAGES (the free list ran out, or
  * free_used is outside [0, n_free]: block-table entry -1, slots[t] = -1),
  * MLA_DEVFLAG_BAD_PAGE (a page id outside [0, num_pages): slots[t] = -1),
  * MLA_DEVFLAG_BAD_TREE (parents[t] < -1 or >= i: the token starts a branch),

@@ -31,7 +31,7 @@ constexpr int kTabWarps = kTabThreads / 32;
 constexpr int kSlice = 128;
 
 struct Request {
-  int ctx, n;       // cached and new tokens (0, 0 where the lengths are wrong)
+  int ctx, n;       // cached and new tokens (a refused request: its cached ones, if those are in order, and 0)
   int have, want;   // pages before and after
   bool bad;
 };
@@ -42,23 +42,37 @@ __device__ __forceinline__ int page_of(const TablesArgs& a, int p) {
   return a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
 }
 
+// A refused request is as it was, so that the step's outputs can be the next
+// one's inputs: the pages that it holds stay its own (without pages_held nothing
+// says which those are), and so does its length where that is in order itself.
 __device__ __forceinline__ Request request(const TablesArgs& a, int b) {
   Request r;
   r.ctx = a.ctx_lens[b];
   r.n = a.new_lens[b];
   const int max_len = a.max_pages * a.page_size;
-  r.bad = r.ctx < 0 || r.n < 0 || r.ctx > max_len || r.n > max_len - r.ctx;
+  bool keep = r.ctx >= 0 && r.ctx <= max_len;  // the length is in order
+  r.bad = !keep || r.n < 0 || r.n > max_len - r.ctx;
+  r.have = !keep || r.ctx == 0 ? 0 : page_of(a, r.ctx - 1) + 1;
+  if (a.pages_held != nullptr) {
+    const int held = a.pages_held[b];
+    keep = keep && held >= r.have && held <= a.max_pages;
+    r.bad = r.bad || !keep;
+    r.have = held;
+  }
   if (!r.bad) {
     const int L = r.ctx + r.n;
-    r.have = r.ctx == 0 ? 0 : page_of(a, r.ctx - 1) + 1;
-    if (a.pages_held != nullptr) {
-      const int held = a.pages_held[b];
-      r.bad = held < r.have || held > a.max_pages;
-      r.have = held;
-    }
     r.want = max(r.have, L == 0 ? 0 : page_of(a, L - 1) + 1);
+    return r;
   }
-  if (r.bad) r.ctx = r.n = r.have = r.want = 0;
+  if (a.pages_held == nullptr) {
+    keep = false;
+    r.have = 0;
+  } else if (r.have < 0 || r.have > a.max_pages) {
+    r.have = 0;
+  }
+  if (!keep) r.ctx = 0;
+  r.n = 0;
+  r.want = r.have;
   return r;
 }
 
