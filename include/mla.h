@@ -409,7 +409,8 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  *   block_table[b][k] = free_pages[free_used + sum_{a<b} (want_a - have_a) + k - have_b]
  *                       for have_b <= k < want_b; other entries stay as they are
  *   free_used_out = free_used + sum_b (want_b - have_b)
- *   seqlens[b] = ctx_b + new_b;  pages_held_out[b] = want_b
+ *   seqlens[b] = ctx_b + new_b
+ *   pages_held_out[b] = want_b, less the pages that the free list did not have
  *   cu_new[b] = sum_{a<b} new_a  (cu_new[B] is the total)
  * and for the new token t = cu_new[b] + i:
  *   seq_ids[t] = b
@@ -430,8 +431,10 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  * that the outputs can be carried on: pages_held_out[b] = pages_held[b] if the
  * block table is that wide, else 0, and seqlens[b] = ctx_b if ctx_b and
  * pages_held[b] are in order, else 0; without pages_held seqlens[b] = 0),
- * MLA_DEVFLAG_NO_PAGES (the free list ran out, or
- * free_used is outside [0, n_free]: block-table entry -1, slots[t] = -1),
+ * MLA_DEVFLAG_NO_PAGES (the free list ran out, or free_used is outside
+ * [0, n_free]: block-table entry -1, slots[t] = -1; seqlens[b] counts the tokens
+ * all the same, so a later step takes the request up from ctx_lens[b], with
+ * pages_held_out[b], and gets the pages that were missing),
  * MLA_DEVFLAG_BAD_PAGE (a page id outside [0, num_pages): slots[t] = -1),
  * MLA_DEVFLAG_BAD_TREE (parents[t] < -1 or >= i: the token starts a branch),
  * MLA_DEVFLAG_NO_ROOM (the total exceeds max_tokens; the tokens past it are

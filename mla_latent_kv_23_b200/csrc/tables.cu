@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
       if (i < a.B) {
         const Request r = request(a, i);
         a.seqlens[i] = r.ctx + r.n;
-        if (a.pages_held_out != nullptr) a.pages_held_out[i] = r.want;
+        // held are the pages that the list had; the request's other new
+        // entries are -1 and taken by a later step
+        if (a.pages_held_out != nullptr)
+          a.pages_held_out[i] = r.have + (int)min((long long)(r.want - r.have), max(0ll, a.n_free - ((long long)used + pg[i])));
       }
     }
   }

@@ -105,3 +105,26 @@ def test_any_steps_lose_no_page():
         lens = [max(0, n - int(rng.integers(0, 30))) for n in want]
         held, used = s["held"], s["used"]
     assert refused > 100 and max(held) == MAX_PAGES
+
+
+def test_pages_that_ran_out_are_not_held():
+    # five of eight pages: the last request gets two of its five
+    table = torch.full((3, 5), -1, dtype=torch.int32, device="cuda")
+    s, slots, cu, f = tables(table, [9, 3, 7, 5, 1], [0, 0, 0], [100, 10, 300], [0, 0, 0], 0)
+    assert f == mla.DEVFLAG_NO_PAGES
+    assert s == dict(lens=[100, 10, 300], held=[2, 1, 2], used=5)
+    assert table.tolist() == [[9, 3, -1, -1, -1], [7, -1, -1, -1, -1], [5, 1, -1, -1, -1]]
+    assert slots[110:410] == rows(table, 2, 0, 128) + [-1] * 172
+    # again with a longer list, from the lengths before: it keeps the two and gets three more
+    s, slots, _, f = tables(table, [9, 3, 7, 5, 1, 8, 6, 4, 2], [100, 10, 0], [0, 0, 300], s["held"], s["used"])
+    assert f == 0 and s == dict(lens=[100, 10, 300], held=[2, 1, 5], used=8)
+    assert table.tolist()[2] == [5, 1, 8, 6, 4] and slots[:300] == rows(table, 2, 0, 300)
+
+
+def test_nothing_free_adds_no_page():
+    for used in (2, 5, -1):  # the list is used up, or its count is out of range
+        table = torch.full((2, 5), -1, dtype=torch.int32, device="cuda")
+        table[:, 0] = i32([11, 12])
+        s, _, _, f = tables(table, [9, 3], [64, 60], [200, 4], [1, 1], used)
+        assert f == mla.DEVFLAG_NO_PAGES and s == dict(lens=[264, 64], held=[1, 1], used=2)
+        assert table.tolist() == [[11, -1, -1, -1, -1], [12, -1, -1, -1, -1]]
