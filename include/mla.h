@@ -537,11 +537,14 @@ mla_status mla_decode_tree(const mla_tree_params* p, void* workspace, size_t wor
  * their places, and `path` gathers whatever else belongs to them.  Whole rows are
  * moved as they are; rows of the cache that are no target keep their values.
  * seqlens_out may be seqlens.
- * Device flags: MLA_DEVFLAG_BAD_TREE (cu_q out of order or outside [0, T], more
- * than 64 drafted tokens, accepted[b] outside [-1, n_b): nothing is kept),
- * MLA_DEVFLAG_BAD_SEQLEN (seqlens[b] < n_b or past the block table: nothing is
- * done, seqlens_out[b] = seqlens[b]), MLA_DEVFLAG_BAD_PAGE (the row is not
- * moved).
+ * Device flags, and what is done with the sequence:
+ *   MLA_DEVFLAG_BAD_TREE, cu_q out of order or outside [0, T] or more than 64
+ *     drafted tokens: nothing; its path and cache rows keep their values,
+ *     seqlens_out[b] = seqlens[b] (the drafted tokens still counted)
+ *   MLA_DEVFLAG_BAD_TREE, accepted[b] outside [-1, n_b): as with -1
+ *   MLA_DEVFLAG_BAD_SEQLEN, seqlens[b] < n_b or past the block table: its path
+ *     is -1, its cache rows keep their values, seqlens_out[b] = seqlens[b]
+ *   MLA_DEVFLAG_BAD_PAGE: the rows on that page are not moved
  */
 typedef struct {
   void* kv_cache;           /* [num_pages * page_size, width] device, read and written */

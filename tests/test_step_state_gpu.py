@@ -128,3 +128,40 @@ def test_nothing_free_adds_no_page():
         s, _, _, f = tables(table, [9, 3], [64, 60], [200, 4], [1, 1], used)
         assert f == mla.DEVFLAG_NO_PAGES and s == dict(lens=[264, 64], held=[1, 1], used=2)
         assert table.tolist() == [[11, -1, -1, -1, -1], [12, -1, -1, -1, -1]]
+
+
+def test_accept_of_wrong_input():
+    before = torch.randn((256, 576), device="cuda").to(torch.bfloat16)
+    mask = torch.full((8,), 0b11010, dtype=torch.int64, device="cuda")
+
+    def accept(cu, lens, accepted):
+        cache, out, path = before.clone(), i32([-7, -7]), i32([-7] * 8)
+        mla.mla_accept_tree(mla.accept_params(cache, i32([[0, 1], [2, 3]]), i32(lens), i32(cu), mask, i32(accepted), out, path, PAGE))
+        f = flags()
+        assert torch.equal(cache, before)
+        return out.tolist(), path.tolist(), f
+
+    # which rows are a tree's is not known: nothing is done for it
+    for cu, accepted in (([0, 9, 8], [3, 1]), ([-1, 4, 2], [3, 1]), ([0, 9, 9], [-1, -1]), ([3, 2, 9], [0, 0])):
+        out, path, f = accept(cu, [100, 50], accepted)
+        assert f == mla.DEVFLAG_BAD_TREE and out == [100, 50] and path == [-7] * 8
+    # its rows in the cache are not known: nothing is kept on the path, the length stays
+    out, path, f = accept([0, 5, 8], [129, 2], [4, 1])
+    assert f == mla.DEVFLAG_BAD_SEQLEN and out == [129, 2] and path == [-1] * 8
+    # only the accepted token is wrong: the tree is dropped
+    out, path, f = accept([0, 5, 8], [100, 50], [5, -2])
+    assert f == mla.DEVFLAG_BAD_TREE and out == [95, 47] and path == [-1] * 8
+
+
+def test_accept_of_a_prompt():
+    # 65 rows are no tree: flagged, and the cache, the path and the length stay
+    cache = torch.randn((256, 576), device="cuda").to(torch.bfloat16)
+    before, mask = cache.clone(), torch.full((68,), 0b110, dtype=torch.int64, device="cuda")
+    out, path = i32([-7, -7]), i32([-7] * 68)
+    mla.mla_accept_tree(mla.accept_params(cache, i32([[0, 1], [2, 3]]), i32([70, 80]), i32([0, 65, 68]), mask,
+                                          i32([-1, 2]), out, path, PAGE))
+    assert flags() == mla.DEVFLAG_BAD_TREE
+    assert out.tolist() == [70, 79] and path.tolist() == [-7] * 65 + [1, 2, -1]
+    want = before.clone()
+    want[128 + 77], want[128 + 78] = before[128 + 78], before[128 + 79]
+    assert torch.equal(cache, want)
