@@ -409,6 +409,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       ++seg_i;
     }
+    // commits of the last tiles and of the last segment, on their way to this CTA
+    for (int k = max(0, g - 2); ok && k < g; ++k) ok = warp_sleep(bar(K_EMPTY + (k & 1)), (k >> 1) & 1, p.err);
+    if (ok && seg_i > 0) warp_sleep(bar(Q_EMPTY), (seg_i - 1) & 1, p.err);
   } else if (warp == kWarpV) {
     // ------------------------------------------------------------ V copies
     // a sequence of one row block reads each of its tiles for the last time
@@ -460,6 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // consumed by the MMAs before the final cluster barrier)
     for (int s = 0; s < 2; ++s)
       if ((local_used >> s) & 1) warp_wait(bar(V_LOCAL + s), ((local_phase >> s) & 1) ^ 1, p.err);
+    // and the commits of the last tiles
+    for (int k = max(0, g - 2); ok && k < g; ++k)
+      ok = warp_sleep(bar(V_EMPTY + (k & 1)), (k >> 1) & 1, p.err) && warp_sleep(bar(PV_DONE + (k & 1)), (k >> 1) & 1, p.err);
   } else if (warp == kWarpMma || warp == kWarpAlloc) {
     // ------------------------------------------------------------ MMA issuers
     // Warp 1 issues every S, warp 2 (done allocating) every P . C.  The two
@@ -549,6 +555,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         g0 += n_t;
         ++seg_i;
+      }
+      // The odd CTA's last signals: no product waits for them, but they are
+      // writes to this CTA's shared memory, and a cluster barrier does not wait
+      // for those (st.async)
+      if (s_issuer) {
+        for (int k = max(0, g0 - 2); ok && k < g0; ++k) ok = wait(S_EMPTY + (k & 1), (k >> 1) & 1);
+      } else if (ok && seg_i > 0) {
+        wait(O_FREE, (seg_i - 1) & 1);
       }
       // every MMA issued by this thread has completed before TMEM is freed
       const int fin = s_issuer ? MMA_FINAL : MMA_FINAL_PV;
@@ -882,7 +896,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // all paired MMAs are complete and no arrival is still on its way
+  // all paired MMAs are complete, and every signal and commit between the CTAs
+  // has been waited for by its receiver: none is still on its way to a CTA that ends
+  cluster_sync();
   if (warp == kWarpAlloc) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
