@@ -404,7 +404,9 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  * captured into a CUDA graph).  Request b has ctx_lens[b] cached tokens and
  * new_lens[b] new ones (drafted tokens, a prompt, or none).  With
  * have_b = ceil(ctx_b / page_size) (or pages_held[b], if given: pages that the
- * request already has, e.g. of drafted tokens that were not accepted) and
+ * request already has, e.g. of drafted tokens that were not accepted; without
+ * it, a length that has become smaller, as mla_accept_tree makes it, loses the
+ * pages behind it) and
  * want_b = max(have_b, ceil((ctx_b + new_b) / page_size)):
  *   block_table[b][k] = free_pages[free_used + sum_{a<b} (want_a - have_a) + k - have_b]
  *                       for have_b <= k < want_b; other entries stay as they are
@@ -435,10 +437,12 @@ mla_status mla_append_latent_slots(const void* h, const void* W_DKV, const void*
  * [0, n_free]: block-table entry -1, slots[t] = -1; seqlens[b] counts the tokens
  * all the same, so a later step takes the request up from ctx_lens[b], with
  * pages_held_out[b], and gets the pages that were missing),
- * MLA_DEVFLAG_BAD_PAGE (a page id outside [0, num_pages): slots[t] = -1),
+ * MLA_DEVFLAG_BAD_PAGE (a page id outside [0, num_pages): slots[t] = -1, a new
+ * block-table entry is -1 and counts as held),
  * MLA_DEVFLAG_BAD_TREE (parents[t] < -1 or >= i: the token starts a branch),
  * MLA_DEVFLAG_NO_ROOM (the total exceeds max_tokens; the tokens past it are
- * dropped, cu_new counts them).
+ * dropped, cu_new and seqlens count them, their pages are held: the step is
+ * taken again as after MLA_DEVFLAG_NO_PAGES).
  * Inputs and outputs must not share a buffer (block_table is extended in
  * place).  B <= 16384.  Pointers 16-byte aligned.  One launch.
  */
@@ -480,8 +484,12 @@ mla_status mla_build_tables(const mla_tables_params* p, void* stream);
  * A token that sees nothing gets u = 0 and lse = -inf.  Cache rows that a token
  * does not see never enter its result, whatever they hold (rows past
  * seqlens[b], and the drafted tokens of other branches, may hold infinities
- * and NaN).  mla_build_tables makes cu_q, seqlens and tree_mask of a tree; a
- * chain of drafted tokens is the mask (2 << r) - 1.
+ * and NaN).  mla_build_tables makes cu_q, seqlens and tree_mask of a step whose
+ * requests have up to 64 new tokens each (longer prompts, which it takes too, are
+ * no trees: here and in mla_accept_tree they raise MLA_DEVFLAG_BAD_TREE, and
+ * their rows are not computed; with the trees first in the batch, both calls can
+ * be given those sequences alone, by B).  A chain of drafted tokens is the mask
+ * (2 << r) - 1.
  *
  * Rows of q, u and lse past cu_q[B] are not read for any result and not
  * written.  Sequences without drafted tokens (n_b = 0) are skipped.  What the

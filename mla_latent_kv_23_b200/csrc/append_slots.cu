@@ -11,8 +11,8 @@
 // tokens all of a CTA's blocks are in flight at once.  The partial tiles (fp32)
 // meet through distributed shared memory: a rank sums its share of the tile over
 // the ranks in order (the result does not depend on timing, and no scratch
-// memory is needed), rotates the RoPE features and writes 16-byte-aligned runs
-// of cache rows.
+// memory is needed), rotates the RoPE features and writes runs of four features
+// (8 bytes a thread, neighbours side by side) of cache rows.
 //
 // fp32: one CTA per token and 32 features on the CUDA cores.
 #include <cuda_bf16.h>
@@ -371,10 +371,12 @@ cudaError_t launch_append_slots(const AppendSlotsArgs& a, const CUtensorMap& w_d
   const int token_tiles = (a.T + kTokens - 1) / kTokens, kb = a.d_model / 64;
   // Boxes per CTA and CTAs along K, by what was measured (us): a block of 64
   // columns takes 0.22 or its bytes at 130 per ns, the exchange of the partial
-  // tile its bytes at 25 per ns, the rest 5.  At d_model = 7168 the model is
-  // within 10 % of the best and of the runners-up: 37 tokens 8.5 with (2 boxes,
-  // 8 CTAs) against 10.6 with (1, 4) and (6, 8); 1024 tokens 17.9 with (6, 4),
-  // 19.8 with (2, 2), 27.5 with (6, 2).
+  // tile its bytes at 25 per ns, the rest 5.  At d_model = 7168 it comes within
+  // 15 % of what one wave of CTAs takes and of what several do, and takes the
+  // fastest of these: 37 tokens 7.5 with (2 boxes, 8 CTAs), 8.2 with (3, 8),
+  // 9.8 with (6, 8), 9.9 with (1, 4); 1024 tokens 16.1 with (5, 4), 18.0 with
+  // (6, 4), 19.2 with (2, 2), 21.5 with (9, 4), 27.7 with (6, 2); 4096 tokens
+  // 38.3 with (9, 2), 45.9 with (9, 4), 47.3 with (5, 2).
   int cs = 1;
   p.boxes = 1;
   double best = 0;

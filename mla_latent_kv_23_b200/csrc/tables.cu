@@ -21,7 +21,7 @@ namespace {
 // of consecutive requests each) into shared memory, and its warps then take
 // jobs of two kinds:
 //   request b:     its new block-table entries and, if it is a drafted tree,
-//                  positions and masks of its tokens;
+//                  positions and masks of its tokens (a prompt: masks of 0);
 //   token slice k: sequence, row and (where the request is no tree) position of
 //                  tokens [128 k, 128 k + 128), four per lane.
 // A new page is read from the free list wherever it is needed, so no job waits
